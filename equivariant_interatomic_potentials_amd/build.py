@@ -37,7 +37,8 @@ CFLAGS = [
 def units():
     """(source, object, extra flags) for every translation unit."""
     out = []
-    for name in ("etp_api", "etp_sh", "etp_graph", "etp_mix", "etp_forces", "etp_neighbors", "etp_node_product"):
+    for name in ("etp_api", "etp_sh", "etp_graph", "etp_mix", "etp_forces", "etp_neighbors", "etp_node_product",
+                 "etp_dense_api", "etp_linear", "etp_layer_norm", "etp_orth"):
         out.append((os.path.join(CSRC, name + ".hip"), os.path.join(BUILD, name + ".o"), []))
     for L in range(5):
         out.append((os.path.join(CSRC, "etp_edge_tp.hip"), os.path.join(BUILD, f"etp_edge_tp_L{L}.o"),
