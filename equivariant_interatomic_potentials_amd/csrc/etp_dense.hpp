@@ -145,9 +145,10 @@ struct OrthArgs {
 size_t orthogonalize_workspace_bytes(int B, int rows, int cols, bool bf16);
 hipError_t launch_orthogonalize(const OrthArgs &a, hipStream_t stream);
 
-// out[i] (+)= sum over s < n of part[s * stride + i], i < count, in order of
-// s (partial sums of weight gradients; n = 0 writes zeros).
-hipError_t launch_sum_parts(int64_t count, int n, int64_t stride, const float *part, float *out, bool accumulate,
-                            hipStream_t stream);
+// Sums of n sets of partial column sums: a set is n0 values that add up to
+// out0 and n1 more for out1 (either output may be null: not written); n = 0
+// writes zeros. Accumulating adds to what the outputs hold.
+hipError_t launch_sum_parts(int64_t n0, float *out0, int64_t n1, float *out1, int n, const float *part,
+                            bool accumulate, hipStream_t stream);
 
 }  // namespace etp

@@ -1,0 +1,219 @@
+// etp_dense_mma.hpp -- matrix-core fragments of the dense operators.
+//
+// Every product runs on v_mfma_f32_16x16x32_bf16: lane (c = lane % 16,
+// q = lane / 16) holds entries k = 8 q .. 8 q + 7 of row c of the first and of
+// column c of the second operand, and rows 4 q .. 4 q + 3 of column c of the
+// float result. A float operand is cut exactly into three bf16 parts
+// (v = p0 + p1 + p2, 8 significant bits each, by truncation, so that no part
+// overflows), and the six products of parts i, j with i + j <= 2 are added in
+// float: the dropped ones are below 2^-22 of |v w|, about a float product's
+// own rounding, at six bf16 instructions of 16 cycles for 8192 products where
+// the fp32 instruction takes 256 cycles.
+#pragma once
+#include "etp_dense.hpp"
+
+namespace etp {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// the same with the element's alignment only (global memory takes any)
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+// bf16 parts that hold a stored value of T exactly
+template <typename T>
+constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+
+template <int P>
+struct Frag {
+    bf16x8 p[P];
+};
+
+__device__ __forceinline__ uint32_t high_halves(float hi, float lo)
+{
+    return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+
+__device__ __forceinline__ float below_high(float v) { return v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
+
+// Eight floats as P bf16 parts each; P = 3 is exact, P = 2 leaves 2^-16 |v|.
+template <int P>
+__device__ __forceinline__ Frag<P> split8(const float (&v)[8])
+{
+    Frag<P> f;
+    uint32_t u[P][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            u[p][i] = high_halves(b, a);
+            if (p + 1 < P) {
+                a = below_high(a);
+                b = below_high(b);
+            }
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+        f.p[p] = __builtin_bit_cast(bf16x8, u32x4{u[p][0], u[p][1], u[p][2], u[p][3]});
+    return f;
+}
+
+// Eight consecutive stored values, the ones from `valid` on zero (not read).
+__device__ __forceinline__ void load8(const float *p, int valid, float (&v)[8])
+{
+    if (valid >= 8) {
+        const f32x4 a = *reinterpret_cast<const f32x4_any *>(p), b = *reinterpret_cast<const f32x4_any *>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = i < valid ? p[i] : 0.f;
+    }
+}
+
+__device__ __forceinline__ u32x4 load8(const bf16bits *p, int valid)
+{
+    if (valid >= 8)
+        return *reinterpret_cast<const u32x4_any *>(p);
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        h[i] = i < valid ? p[i] : 0u;
+    return u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+}
+
+__device__ __forceinline__ void load8(const bf16bits *p, int valid, float (&v)[8])
+{
+    const u32x4 u = load8(p, valid);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+
+// Eight stored values as loaded, turned into floats where they are used (so
+// that nothing waits for the load before that).
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float *p, int valid) { load8(p, valid, v); }
+    __device__ __forceinline__ void get(float (&o)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] = v[i];
+    }
+    template <int P>
+    __device__ __forceinline__ Frag<P> frag() const
+    {
+        return split8<P>(v);
+    }
+};
+template <>
+struct Raw8<bf16bits> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const bf16bits *p, int valid) { v = load8(p, valid); }
+    __device__ __forceinline__ void get(float (&o)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = __uint_as_float(v[i] << 16);
+            o[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+        }
+    }
+    template <int P>
+    __device__ __forceinline__ Frag<P> frag() const
+    {
+        static_assert(P == 1, "a bf16 value is one part");
+        return {{__builtin_bit_cast(bf16x8, v)}};
+    }
+};
+
+// Writes eight consecutive values, the first `valid` of them.
+__device__ __forceinline__ void store8(float *p, int valid, const float (&v)[8])
+{
+    if (valid >= 8) {
+        *reinterpret_cast<f32x4_any *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4_any *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < valid)
+                p[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ void store8(bf16bits *p, int valid, const float (&v)[8])
+{
+    if (valid >= 8) {
+        u32x4 u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            u[i] = from_f32<bf16bits>(v[2 * i]) | static_cast<uint32_t>(from_f32<bf16bits>(v[2 * i + 1])) << 16;
+        *reinterpret_cast<u32x4_any *>(p) = u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < valid)
+                p[i] = from_f32<bf16bits>(v[i]);
+    }
+}
+
+// Four or eight consecutive values (v holds eight).
+template <int N, typename T>
+__device__ __forceinline__ void load_n(const T *p, int valid, float (&v)[8])
+{
+    if constexpr (N == 8) {
+        load8(p, valid, v);
+    } else if (valid >= 4) {
+        const f32x4 a = *reinterpret_cast<const f32x4_any *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = a[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = i < valid ? p[i] : 0.f;
+    }
+}
+
+template <int N, typename T>
+__device__ __forceinline__ void store_n(T *p, int valid, const float (&v)[8])
+{
+    if constexpr (N == 8) {
+        store8(p, valid, v);
+    } else if (valid >= 4) {
+        *reinterpret_cast<f32x4_any *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < valid)
+                p[i] = v[i];
+    }
+}
+
+// acc += the products of parts i of a and j of b with i + j <= 2, the
+// smallest first.
+template <int PA, int PB>
+__device__ __forceinline__ f32x4 mma(const Frag<PA> &a, const Frag<PB> &b, f32x4 acc)
+{
+#pragma unroll
+    for (int s = (PA + PB - 2 < 2 ? PA + PB - 2 : 2); s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < PA; ++i)
+            if (s - i >= 0 && s - i < PB)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], acc, 0, 0, 0);
+    return acc;
+}
+
+}  // namespace etp

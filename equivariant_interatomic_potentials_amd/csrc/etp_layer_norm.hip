@@ -1,40 +1,330 @@
 // etp_layer_norm.hip -- the layer norm over the columns of each row, and its
 // VJP with the weights' gradients.
-#include "etp_dense.hpp"
+//
+// Both are one pass over the data, bound by HBM. LPR lanes (a power of two up
+// to the wave) own a row and hold it in registers, 16 bytes a load, so that
+// mean, variance (from the differences) and the result come from one read;
+// sums over the row are exchanges between the LPR lanes. A lane keeps the same
+// columns for every row it meets, so gamma and beta are read once and the
+// VJP's column sums grow in registers; waves walk the rows with the grid's
+// stride and load the next row while they work on the present one. Rows of
+// more than 2048 columns take a workgroup each and read the row again (from
+// cache) for every sum.
+#include "etp_dense_mma.hpp"
 
 namespace etp {
 
-__device__ __forceinline__ float wave_sum_xor(float v)
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+
+// A vector of kVec values as loaded, turned into floats where they are used.
+template <typename T>
+struct RawVec;
+template <>
+struct RawVec<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float *p, int valid) { load_n<4>(p, valid, v); }
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+};
+template <>
+struct RawVec<bf16bits> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const bf16bits *p, int valid) { v = load8(p, valid); }
+    __device__ __forceinline__ float get(int i) const
+    {
+        return __uint_as_float(i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+    }
+};
+
+template <int Ctrl>
+__device__ __forceinline__ float dpp_add(float v)
 {
-#pragma unroll
-    for (int m = 32; m; m >>= 1)
-        v += __shfl_xor(v, m);
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), Ctrl, 0xF, 0xF, true));
+}
+
+// Sum over aligned groups of N lanes, in every lane of the group.
+template <int N>
+__device__ __forceinline__ float group_sum(float v)
+{
+    if constexpr (N >= 2)
+        v = dpp_add<0xB1>(v);  // quad_perm 1,0,3,2
+    if constexpr (N >= 4)
+        v = dpp_add<0x4E>(v);  // quad_perm 2,3,0,1
+    if constexpr (N >= 8)
+        v = dpp_add<0x141>(v);  // row_half_mirror
+    if constexpr (N >= 16)
+        v = dpp_add<0x140>(v);  // row_mirror
+    if constexpr (N >= 32)
+        v += __shfl_xor(v, 16);
+    if constexpr (N >= 64)
+        v += __shfl_xor(v, 32);
     return v;
 }
 
-// a wave per row
-template <typename T>
+// s / c from inv = 1 / c with one correction, so that a quotient that is a
+// float comes out exactly (the mean of a constant row is its value).
+__device__ __forceinline__ float quotient(float s, float c, float inv)
+{
+    const float m = s * inv;
+    return __builtin_fmaf(__builtin_fmaf(-m, c, s), inv, m);
+}
+
+// The columns of lane l of a row's LPR lanes: vector n holds kVec columns
+// from col[n], its own ones the entries [lo[n], hi). The last vector of a
+// ragged row is moved back to end at the row's end (its first entries belong
+// to the vector before it), so that every load is a whole vector; only rows
+// shorter than a vector are loaded by parts.
+template <typename T, int LPR, int NI, bool RAG>
+struct Columns {
+    int col[NI], lo[NI], hi;
+    __device__ __forceinline__ Columns(int l, int C)
+    {
+        constexpr int V = kVec<T>;
+        hi = RAG && C < V ? C : V;
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const int want = (n * LPR + l) * V;
+            const int last = C > V ? C - V : 0;
+            col[n] = RAG && want > last ? last : want;
+            lo[n] = RAG ? (want - col[n] < V ? want - col[n] : V) : 0;
+        }
+    }
+    __device__ __forceinline__ bool own(int n, int i) const { return !RAG || (i >= lo[n] && i < hi); }
+    // row: the row's first element; entries that are not own hold anything
+    __device__ __forceinline__ void load(const T *row, int n, RawVec<T> &v) const { v.load(row + col[n], hi); }
+    __device__ __forceinline__ void store(T *row, int n, const float (&v)[8]) const
+    {
+        constexpr int V = kVec<T>;
+        if (!RAG || (lo[n] == 0 && hi == V)) {
+            store_n<V>(row + col[n], V, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (own(n, i))
+                    row[col[n] + i] = from_f32<T>(v[i]);
+        }
+    }
+    __device__ __forceinline__ float weight(const float *w, int n, int i, float none) const
+    {
+        return w && own(n, i) ? w[col[n] + i] : none;
+    }
+};
+
+template <typename T, int LPR, int NI, bool RAG>
 __global__ void __launch_bounds__(256) layer_norm_kernel(const NormArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    for (int64_t r = blockIdx.x * 4ll + (threadIdx.x >> 6); r < a.M; r += gridDim.x * 4ll) {
+    constexpr int V = kVec<T>, RPW = 64 / LPR;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const Columns<T, LPR, NI, RAG> cs(lane % LPR, a.C);
+    float gamma[NI][V], beta[NI][V];
+#pragma unroll
+    for (int n = 0; n < NI; ++n)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            gamma[n][i] = cs.weight(a.gamma, n, i, 1.f);
+            beta[n][i] = cs.weight(a.beta, n, i, 0.f);
+        }
+    const float inv = 1.f / static_cast<float>(a.C);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * RPW;
+    int64_t r = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * RPW + lane / LPR;
+    float x[NI][V];
+    RawVec<T> nx[NI];
+    auto fetch = [&](int64_t row) {
+        const T *p = static_cast<const T *>(a.x) + (row < a.M ? row : a.M - 1) * a.ldx;
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+            cs.load(p, n, nx[n]);
+    };
+    fetch(r);
+    for (int64_t r0 = r - lane / LPR; r0 < a.M; r0 += step, r += step) {
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                x[n][i] = nx[n].get(i);
+        if (r0 + step < a.M)
+            fetch(r + step);
+        float s = 0.f;
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                s += cs.own(n, i) ? x[n][i] : 0.f;
+        const float mean = quotient(group_sum<LPR>(s), static_cast<float>(a.C), inv);
+        float v = 0.f;
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[n][i] = cs.own(n, i) ? x[n][i] - mean : 0.f;
+                v = __builtin_fmaf(x[n][i], x[n][i], v);
+            }
+        const float rstd = 1.f / sqrtf(__builtin_fmaf(group_sum<LPR>(v), inv, a.eps));
+        if (r >= a.M)
+            continue;
+        T *y = static_cast<T *>(a.y) + r * a.ldy;
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                o[i] = __builtin_fmaf(x[n][i] * rstd, gamma[n][i], beta[n][i]);
+            cs.store(y, n, o);
+        }
+        if (lane % LPR == 0) {
+            if (a.mean)
+                a.mean[r] = mean;
+            if (a.rstd)
+                a.rstd[r] = rstd;
+        }
+    }
+}
+
+// Input gradient and this workgroup's column sums, part[b][0][c] = sum gy h,
+// part[b][1][c] = sum gy over its rows: lanes, then the wave's row groups,
+// then the four waves, in a fixed order.
+template <typename T, int LPR, int NI, bool RAG>
+__global__ void __launch_bounds__(256) layer_norm_vjp_kernel(const NormVjpArgs a)
+{
+    constexpr int V = kVec<T>, RPW = 64 / LPR;
+    __shared__ float sums[4][2][LPR * NI * V];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const Columns<T, LPR, NI, RAG> cs(lane % LPR, a.C);
+    float gamma[NI][V], gg[NI][V], gb[NI][V];
+#pragma unroll
+    for (int n = 0; n < NI; ++n)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            gamma[n][i] = cs.weight(a.gamma, n, i, 1.f);
+            gg[n][i] = gb[n][i] = 0.f;
+        }
+    const float inv = 1.f / static_cast<float>(a.C);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * RPW;
+    int64_t r = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * RPW + lane / LPR;
+    RawVec<T> nx[NI], ng[NI];
+    float nmean, nrstd;
+    auto fetch = [&](int64_t row) {
+        const int64_t rc = row < a.M ? row : a.M - 1;
+        const T *p = static_cast<const T *>(a.x) + rc * a.ldx, *g = static_cast<const T *>(a.gy) + rc * a.ldgy;
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            cs.load(p, n, nx[n]);
+            cs.load(g, n, ng[n]);
+        }
+        nmean = a.mean[rc];
+        nrstd = a.rstd[rc];
+    };
+    fetch(r);
+    for (int64_t r0 = r - lane / LPR; r0 < a.M; r0 += step, r += step) {
+        float h[NI][V], g[NI][V];
+        const float mean = nmean, rstd = nrstd;
+        const bool live = r < a.M;
+        float s = 0.f, t = 0.f;
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const bool own = live && cs.own(n, i);
+                g[n][i] = own ? ng[n].get(i) : 0.f;
+                h[n][i] = own ? (nx[n].get(i) - mean) * rstd : 0.f;
+            }
+        if (r0 + step < a.M)
+            fetch(r + step);
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                gg[n][i] = __builtin_fmaf(g[n][i], h[n][i], gg[n][i]);
+                gb[n][i] += g[n][i];
+                g[n][i] *= gamma[n][i];
+                s += g[n][i];
+                t = __builtin_fmaf(g[n][i], h[n][i], t);
+            }
+        if (!a.gx)
+            continue;
+        s = group_sum<LPR>(s) * inv;
+        t = group_sum<LPR>(t) * inv;
+        if (!live)
+            continue;
+        T *gx = static_cast<T *>(a.gx) + r * a.ldgx;
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            float o[8];
+            RawVec<T> was;
+            if (a.accumulate)
+                cs.load(gx, n, was);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                o[i] = rstd * (g[n][i] - s - h[n][i] * t);
+                if (a.accumulate)
+                    o[i] += was.get(i);
+            }
+            cs.store(gx, n, o);
+        }
+    }
+    if (!a.ws)
+        return;
+#pragma unroll
+    for (int n = 0; n < NI; ++n)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float u = gg[n][i], w = gb[n][i];
+#pragma unroll
+            for (int m = LPR; m < 64; m <<= 1) {
+                u += __shfl_xor(u, m);
+                w += __shfl_xor(w, m);
+            }
+            if (lane < LPR) {
+                sums[wave][0][(n * LPR + lane) * V + i] = u;
+                sums[wave][1][(n * LPR + lane) * V + i] = w;
+            }
+        }
+    __syncthreads();
+    float *part = static_cast<float *>(a.ws) + static_cast<int64_t>(blockIdx.x) * 2 * a.C;
+    for (int k = threadIdx.x; k < 2 * LPR * NI * V; k += 256) {
+        const int w = k >= LPR * NI * V, e = k - w * LPR * NI * V;
+        const int want = e / V * V, last = a.C > V ? a.C - V : 0;
+        const int c = (RAG && want > last ? last : want) + e % V;  // the vector's column (Columns)
+        if (c >= want && c < a.C)
+            part[w * a.C + c] = (sums[0][w][e] + sums[1][w][e]) + (sums[2][w][e] + sums[3][w][e]);
+    }
+}
+
+// --------------------------------------------------------------- long rows
+
+// sum over the workgroup's 256 threads, in every thread
+__device__ __forceinline__ float block_sum(float v, float *lds)
+{
+    v = group_sum<64>(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) layer_norm_long_kernel(const NormArgs a)
+{
+    __shared__ float lds[4];
+    const float inv = 1.f / static_cast<float>(a.C);
+    for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
         const T *x = static_cast<const T *>(a.x) + r * a.ldx;
         float s = 0.f;
-        for (int c = lane; c < a.C; c += 64)
+        for (int c = threadIdx.x; c < a.C; c += 256)
             s += to_f32(x[c]);
-        const float mean = wave_sum_xor(s) / a.C;
+        const float mean = quotient(block_sum(s, lds), static_cast<float>(a.C), inv);
         float q = 0.f;
-        for (int c = lane; c < a.C; c += 64) {
+        for (int c = threadIdx.x; c < a.C; c += 256) {
             const float d = to_f32(x[c]) - mean;
             q = __builtin_fmaf(d, d, q);
         }
-        const float rstd = 1.f / sqrtf(wave_sum_xor(q) / a.C + a.eps);
+        const float rstd = 1.f / sqrtf(__builtin_fmaf(block_sum(q, lds), inv, a.eps));
         T *y = static_cast<T *>(a.y) + r * a.ldy;
-        for (int c = lane; c < a.C; c += 64) {
-            const float h = (to_f32(x[c]) - mean) * rstd;
-            y[c] = from_f32<T>(__builtin_fmaf(h, a.gamma ? a.gamma[c] : 1.f, a.beta ? a.beta[c] : 0.f));
-        }
-        if (lane == 0) {
+        for (int c = threadIdx.x; c < a.C; c += 256)
+            y[c] = from_f32<T>(__builtin_fmaf((to_f32(x[c]) - mean) * rstd, a.gamma ? a.gamma[c] : 1.f,
+                                              a.beta ? a.beta[c] : 0.f));
+        if (threadIdx.x == 0) {
             if (a.mean)
                 a.mean[r] = mean;
             if (a.rstd)
@@ -44,22 +334,23 @@ __global__ void __launch_bounds__(256) layer_norm_kernel(const NormArgs a)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) layer_norm_gx_kernel(const NormVjpArgs a)
+__global__ void __launch_bounds__(256) layer_norm_long_gx_kernel(const NormVjpArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    for (int64_t r = blockIdx.x * 4ll + (threadIdx.x >> 6); r < a.M; r += gridDim.x * 4ll) {
+    __shared__ float lds[4];
+    const float inv = 1.f / static_cast<float>(a.C);
+    for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
         const T *x = static_cast<const T *>(a.x) + r * a.ldx, *gy = static_cast<const T *>(a.gy) + r * a.ldgy;
         const float mean = a.mean[r], rstd = a.rstd[r];
         float s = 0.f, t = 0.f;
-        for (int c = lane; c < a.C; c += 64) {
+        for (int c = threadIdx.x; c < a.C; c += 256) {
             const float h = (to_f32(x[c]) - mean) * rstd, d = to_f32(gy[c]) * (a.gamma ? a.gamma[c] : 1.f);
             s += d;
             t = __builtin_fmaf(d, h, t);
         }
-        s = wave_sum_xor(s) / a.C;
-        t = wave_sum_xor(t) / a.C;
+        s = block_sum(s, lds) * inv;
+        t = block_sum(t, lds) * inv;
         T *gx = static_cast<T *>(a.gx) + r * a.ldgx;
-        for (int c = lane; c < a.C; c += 64) {
+        for (int c = threadIdx.x; c < a.C; c += 256) {
             const float h = (to_f32(x[c]) - mean) * rstd, d = to_f32(gy[c]) * (a.gamma ? a.gamma[c] : 1.f);
             const float g = rstd * (d - s - h * t);
             gx[c] = from_f32<T>(a.accumulate ? to_f32(gx[c]) + g : g);
@@ -69,7 +360,7 @@ __global__ void __launch_bounds__(256) layer_norm_gx_kernel(const NormVjpArgs a)
 
 // part[s][0][c] = sum over the rows of split s of gy h, part[s][1][c] of gy
 template <typename T>
-__global__ void __launch_bounds__(256) layer_norm_gw_kernel(const NormVjpArgs a, const int nsplit)
+__global__ void __launch_bounds__(256) layer_norm_long_gw_kernel(const NormVjpArgs a, const int nsplit)
 {
     const int c = blockIdx.x * 256 + threadIdx.x, s = blockIdx.y;
     if (c >= a.C)
@@ -87,58 +378,115 @@ __global__ void __launch_bounds__(256) layer_norm_gw_kernel(const NormVjpArgs a,
     part[a.C + c] = gb;
 }
 
-static unsigned row_grid(int64_t M)
+// ----------------------------------------------------------------- dispatch
+
+constexpr int kLongRow = 2048;
+
+// Calls f<LPR, NI, RAG>() for rows of C <= 2048 columns in vectors of V.
+template <int V, typename F>
+static hipError_t by_columns(int C, F &&f)
 {
-    const int64_t b = (M + 3) / 4;
-    return static_cast<unsigned>(b < 8192 ? b : 8192);
+    const int vecs = (C + V - 1) / V;
+#define ETP_NORM_CASE(L, N)                                                                      \
+    if (vecs <= L * N)                                                                           \
+        return C == L * N * V ? f(std::integral_constant<int, L>{}, std::integral_constant<int, N>{}, \
+                                  std::false_type{})                                             \
+                              : f(std::integral_constant<int, L>{}, std::integral_constant<int, N>{}, \
+                                  std::true_type{});
+    ETP_NORM_CASE(1, 1)
+    ETP_NORM_CASE(2, 1)
+    ETP_NORM_CASE(4, 1)
+    ETP_NORM_CASE(8, 1)
+    ETP_NORM_CASE(16, 1)
+    ETP_NORM_CASE(32, 1)
+    ETP_NORM_CASE(64, 1)
+    ETP_NORM_CASE(64, 2)
+    ETP_NORM_CASE(64, 4)
+    if constexpr (V == 4) {
+        ETP_NORM_CASE(64, 8)
+    }
+#undef ETP_NORM_CASE
+    return hipErrorInvalidValue;
+}
+
+// Workgroups of four waves over M rows of which a wave takes rpw at a time.
+static unsigned norm_grid(int64_t M, int rpw, int most)
+{
+    const int64_t b = (M + 4 * rpw - 1) / (4 * rpw);
+    return static_cast<unsigned>(b < most ? b : most);
+}
+
+template <typename T>
+static hipError_t norm_forward(const NormArgs &a, hipStream_t stream)
+{
+    if (a.C > kLongRow) {
+        hipLaunchKernelGGL(layer_norm_long_kernel<T>, dim3(norm_grid(a.M, 1, 2048)), dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
+    return by_columns<kVec<T>>(a.C, [&](auto l, auto n, auto rag) {
+        hipLaunchKernelGGL((layer_norm_kernel<T, l(), n(), rag()>), dim3(norm_grid(a.M, 64 / l(), 2048)), dim3(256), 0,
+                           stream, a);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_layer_norm(const NormArgs &a, hipStream_t stream)
 {
     if (a.M == 0)
         return hipSuccess;
-    if (a.bf16)
-        hipLaunchKernelGGL(layer_norm_kernel<bf16bits>, dim3(row_grid(a.M)), dim3(256), 0, stream, a);
-    else
-        hipLaunchKernelGGL(layer_norm_kernel<float>, dim3(row_grid(a.M)), dim3(256), 0, stream, a);
-    return hipGetLastError();
+    return a.bf16 ? norm_forward<bf16bits>(a, stream) : norm_forward<float>(a, stream);
 }
 
-static int norm_splits(int64_t M)
+// Partial column sums of the VJP: one set per workgroup.
+static int norm_parts(int64_t M, int C, bool bf16)
 {
-    const int64_t s = M / 16;
-    return static_cast<int>(s < 1 ? 1 : s > 512 ? 512 : s);
-}
-
-size_t layer_norm_vjp_workspace_bytes(int64_t M, int C, bool)
-{
-    return M == 0 ? 0 : sizeof(float) * 2 * static_cast<size_t>(norm_splits(M)) * C;
-}
-
-hipError_t launch_layer_norm_vjp(const NormVjpArgs &a, hipStream_t stream)
-{
-    if (a.M > 0 && a.gx) {
-        if (a.bf16)
-            hipLaunchKernelGGL(layer_norm_gx_kernel<bf16bits>, dim3(row_grid(a.M)), dim3(256), 0, stream, a);
-        else
-            hipLaunchKernelGGL(layer_norm_gx_kernel<float>, dim3(row_grid(a.M)), dim3(256), 0, stream, a);
+    if (C > kLongRow) {
+        const int64_t s = M / 16;
+        return static_cast<int>(s < 1 ? 1 : s > 512 ? 512 : s);
     }
-    if (!a.ggamma && !a.gbeta)
+    const int V = bf16 ? 8 : 4, vecs = (C + V - 1) / V;
+    int lpr = 1;
+    while (lpr < 64 && lpr < vecs)
+        lpr *= 2;
+    return static_cast<int>(norm_grid(M, 64 / lpr, 1024));
+}
+
+size_t layer_norm_vjp_workspace_bytes(int64_t M, int C, bool bf16)
+{
+    return M == 0 ? 0 : sizeof(float) * 2 * static_cast<size_t>(norm_parts(M, C, bf16)) * C;
+}
+
+template <typename T>
+static hipError_t norm_vjp(const NormVjpArgs &a, int S, hipStream_t stream)
+{
+    if (a.C > kLongRow) {
+        if (a.gx)
+            hipLaunchKernelGGL(layer_norm_long_gx_kernel<T>, dim3(norm_grid(a.M, 1, 2048)), dim3(256), 0, stream, a);
+        if (a.ws)
+            hipLaunchKernelGGL(layer_norm_long_gw_kernel<T>, dim3(static_cast<unsigned>((a.C + 255) / 256), S),
+                               dim3(256), 0, stream, a, S);
         return hipGetLastError();
-    const int S = a.M == 0 ? 0 : norm_splits(a.M);
-    if (S > 0) {
-        const dim3 grid(static_cast<unsigned>((a.C + 255) / 256), S);
-        if (a.bf16)
-            hipLaunchKernelGGL(layer_norm_gw_kernel<bf16bits>, grid, dim3(256), 0, stream, a, S);
-        else
-            hipLaunchKernelGGL(layer_norm_gw_kernel<float>, grid, dim3(256), 0, stream, a, S);
     }
+    return by_columns<kVec<T>>(a.C, [&](auto l, auto n, auto rag) {
+        hipLaunchKernelGGL((layer_norm_vjp_kernel<T, l(), n(), rag()>), dim3(static_cast<unsigned>(S)), dim3(256), 0,
+                           stream, a);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_layer_norm_vjp(const NormVjpArgs &args, hipStream_t stream)
+{
+    NormVjpArgs a = args;
+    const bool sums = a.ggamma || a.gbeta;
+    if (!sums)
+        a.ws = nullptr;
+    const int S = a.M == 0 ? 0 : norm_parts(a.M, a.C, a.bf16);
+    hipError_t e = hipSuccess;
+    if (S > 0 && (a.gx || sums))
+        e = a.bf16 ? norm_vjp<bf16bits>(a, S, stream) : norm_vjp<float>(a, S, stream);
     const float *part = static_cast<const float *>(a.ws);
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && a.ggamma)
-        e = launch_sum_parts(a.C, S, 2 * a.C, part, a.ggamma, a.accumulate, stream);
-    if (e == hipSuccess && a.gbeta)
-        e = launch_sum_parts(a.C, S, 2 * a.C, part ? part + a.C : nullptr, a.gbeta, a.accumulate, stream);
+    if (e == hipSuccess && sums)
+        e = launch_sum_parts(a.C, a.ggamma, a.C, a.gbeta, S, part, a.accumulate, stream);
     return e;
 }
 

@@ -1,114 +1,872 @@
 // etp_linear.hip -- the linear layer with bias, activation and residual, and
 // its VJP.
-#include "etp_dense.hpp"
+#include <type_traits>
+
+#include "etp_dense_mma.hpp"
 
 namespace etp {
 
-// y = act(x W + bias) + res: a 16 x 16 output tile per workgroup, x and W
-// through LDS in chunks of 16 of the inner dimension.
-template <typename T>
-__global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a)
-{
-    __shared__ float xs[16][17], wsh[16][17];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 16 + ty;
-    const int j = blockIdx.y * 16 + tx;
-    const T *x = static_cast<const T *>(a.x), *W = static_cast<const T *>(a.W);
-    float acc = 0.f;
-    for (int k0 = 0; k0 < a.K; k0 += 16) {
-        xs[ty][tx] = r < a.M && k0 + tx < a.K ? to_f32(x[r * a.ldx + k0 + tx]) : 0.f;
-        wsh[ty][tx] = j < a.N && k0 + ty < a.K ? to_f32(W[static_cast<int64_t>(k0 + ty) * a.N + j]) : 0.f;
-        __syncthreads();
-        for (int k = 0; k < 16; ++k)
-            acc = __builtin_fmaf(xs[ty][k], wsh[k][tx], acc);
-        __syncthreads();
+// ---------------------------------------------------------------------------
+// y = act(x W + bias) + res (forward) and gx = d W^T, d = gy act'(z) (input
+// gradient) are one product: rows r of [M][KD] times a [KD][ND] matrix in
+// float accumulators, with another first operand and another epilogue.
+//
+// Operands are swapped: the matrix is the first operand of the instruction
+// and the rows are the second, so that a lane ends with consecutive columns
+// of one row and stores them as one vector, and loads its eight consecutive
+// k of a row straight from memory (each row of x is needed by one wave only;
+// only the matrix goes through LDS, in fragment order: a lane's 16 bytes next
+// to its neighbours').
+
+// Fwd: rows are x; Gx: rows are gy and z; GxD: rows are d, in float.
+enum class Dense { Fwd, Gx, GxD };
+
+struct ProductArgs {
+    int64_t M;
+    int KD, ND;      // contraction, output columns
+    const void *A;   // rows: x, gy, or d
+    int64_t lda;
+    const void *Z;   // pre-activation (Gx with an activation)
+    int64_t ldz;
+    const void *W;   // [n_in][n_out]: [KD][ND] (Fwd) or [ND][KD] (Gx)
+    const float *bias;
+    int act;
+    const void *res;
+    int64_t ldr;
+    void *out;
+    int64_t ldo;
+    void *zout;
+    int64_t ldzo;
+    bool accumulate;
+};
+
+// Parts of the row operand: a stored float exactly; d of a bf16 layer in two
+// (2^-16 relative, far below the rounding of the bf16 result).
+template <typename T, Dense D>
+constexpr int kRowParts = sizeof(T) == 4 ? 3 : (D == Dense::Fwd ? 1 : 2);
+
+// Eight entries of a row as loaded, and as matrix-core parts.
+template <typename T, Dense D>
+struct RowChunk {
+    Raw8<T> v;
+    __device__ __forceinline__ void load(const ProductArgs &a, int64_t row, int k)
+    {
+        v.load(static_cast<const T *>(a.A) + row * a.lda + k, a.KD - k);
     }
-    if (r >= a.M || j >= a.N)
+    __device__ __forceinline__ Frag<kParts<T>> frag(const ProductArgs &) const
+    {
+        return v.template frag<kParts<T>>();
+    }
+};
+
+template <typename T>
+struct RowChunk<T, Dense::Gx> {
+    Raw8<T> g, z;
+    __device__ __forceinline__ void load(const ProductArgs &a, int64_t row, int k)
+    {
+        g.load(static_cast<const T *>(a.A) + row * a.lda + k, a.KD - k);
+        if (a.act != kActNone)
+            z.load(static_cast<const T *>(a.Z) + row * a.ldz + k, a.KD - k);
+    }
+    __device__ __forceinline__ Frag<kRowParts<T, Dense::Gx>> frag(const ProductArgs &a) const
+    {
+        float d[8];
+        g.get(d);
+        if (a.act != kActNone) {
+            float zv[8];
+            z.get(zv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                d[i] *= act_slope(a.act, zv[i]);
+        }
+        return split8<kRowParts<T, Dense::Gx>>(d);
+    }
+};
+
+template <typename T>
+struct RowChunk<T, Dense::GxD> {
+    Raw8<float> d;
+    __device__ __forceinline__ void load(const ProductArgs &a, int64_t row, int k)
+    {
+        d.load(static_cast<const float *>(a.A) + row * a.lda + k, a.KD - k);
+    }
+    __device__ __forceinline__ Frag<kRowParts<T, Dense::GxD>> frag(const ProductArgs &) const
+    {
+        return d.template frag<kRowParts<T, Dense::GxD>>();
+    }
+};
+
+// A lane's result columns: a float lane stores four columns of a 16-column
+// tile (64 contiguous bytes a row for the wave); a bf16 lane stores eight
+// columns out of a pair of tiles (again 64 bytes), which are interleaved for
+// that: entry c of tile t is column 32 (t / 2) + 8 (c / 4) + 4 (t % 2) + c % 4.
+template <typename T>
+__device__ __forceinline__ int tile_of_col(int j)
+{
+    return sizeof(T) == 4 ? j >> 4 : 2 * (j >> 5) + ((j >> 2) & 1);
+}
+template <typename T>
+__device__ __forceinline__ int entry_of_col(int j)
+{
+    return sizeof(T) == 4 ? j & 15 : 4 * ((j >> 3) & 3) + (j & 3);
+}
+// first of the four consecutive columns that quarter q of tile t holds
+template <typename T>
+__device__ __forceinline__ int col_of_quarter(int t, int q)
+{
+    return sizeof(T) == 4 ? 16 * t + 4 * q : 32 * (t >> 1) + 8 * q + 4 * (t & 1);
+}
+
+// Entries k .. k + 7 of column j of the [KD][ND] matrix as loaded, zero
+// outside, and as matrix-core parts.
+template <typename T, Dense D>
+struct MatrixChunk {
+    T v[8];
+    __device__ __forceinline__ void load(const ProductArgs &a, int k, int j)
+    {
+        const T *W = static_cast<const T *>(a.W);
+        if constexpr (D == Dense::Fwd) {
+            const T *p = W + static_cast<int64_t>(k) * a.ND + j;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = k + i < a.KD && j < a.ND ? p[static_cast<int64_t>(i) * a.ND] : T(0);
+        } else {
+            const T *p = W + static_cast<int64_t>(j < a.ND ? j : 0) * a.KD + k;
+            const int valid = j < a.ND ? a.KD - k : 0;
+            if constexpr (sizeof(T) == 4)
+                load8(p, valid, v);
+            else
+                *reinterpret_cast<u32x4_any *>(v) = load8(p, valid);
+        }
+    }
+    __device__ __forceinline__ Frag<kParts<T>> frag() const
+    {
+        if constexpr (sizeof(T) == 4) {
+            return split8<3>(v);
+        } else {
+            u32x4 u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = v[2 * i] | static_cast<uint32_t>(v[2 * i + 1]) << 16;
+            return {{__builtin_bit_cast(bf16x8, u)}};
+        }
+    }
+};
+
+// Epilogue: NV consecutive columns from j of one row (4 float, 8 bf16).
+template <typename T, Dense D, int NV>
+__device__ __forceinline__ void store_cols(const ProductArgs &a, int64_t row, int j, float (&v)[8], const float (&r)[8])
+{
+    const int valid = a.ND - j;
+    if (valid <= 0)
         return;
-    const float z = acc + (a.bias ? a.bias[j] : 0.f);
-    float y = act_value(a.act, z);
-    if (a.res)
-        y += to_f32(static_cast<const T *>(a.res)[r * a.ldr + j]);
-    static_cast<T *>(a.y)[r * a.ldy + j] = from_f32<T>(y);
-    if (a.z)
-        static_cast<T *>(a.z)[r * a.ldz + j] = from_f32<T>(z);
-}
-
-template <typename T>
-__device__ __forceinline__ float slope_grad(const LinearVjpArgs &a, int64_t r, int j)
-{
-    const float g = to_f32(static_cast<const T *>(a.gy)[r * a.ldgy + j]);
-    return a.act == kActNone ? g : g * act_slope(a.act, to_f32(static_cast<const T *>(a.z)[r * a.ldz + j]));
-}
-
-// gx = d W^T, d = gy act'(z)
-template <typename T>
-__global__ void __launch_bounds__(256) linear_gx_kernel(const LinearVjpArgs a)
-{
-    __shared__ float ds[16][17], wsh[16][17];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 16 + ty;
-    const int k = blockIdx.y * 16 + tx;
-    const T *W = static_cast<const T *>(a.W);
-    float acc = 0.f;
-    for (int j0 = 0; j0 < a.N; j0 += 16) {
-        ds[ty][tx] = r < a.M && j0 + tx < a.N ? slope_grad<T>(a, r, j0 + tx) : 0.f;
-        const int kw = blockIdx.y * 16 + ty;
-        wsh[ty][tx] = kw < a.K && j0 + tx < a.N ? to_f32(W[static_cast<int64_t>(kw) * a.N + j0 + tx]) : 0.f;
-        __syncthreads();
-        for (int j = 0; j < 16; ++j)
-            acc = __builtin_fmaf(ds[ty][j], wsh[tx][j], acc);
-        __syncthreads();
+    if constexpr (D == Dense::Fwd) {
+        if (a.zout)
+            store_n<NV>(static_cast<T *>(a.zout) + row * a.ldzo + j, valid, v);
+        if (a.act != kActNone) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                v[i] = act_value(a.act, v[i]);
+        }
+        if (a.res) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                v[i] += r[i];
+        }
+    } else if (a.accumulate) {  // Gx, GxD
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            v[i] += r[i];
     }
-    if (r >= a.M || k >= a.K)
+    store_n<NV>(static_cast<T *>(a.out) + row * a.ldo + j, valid, v);
+}
+
+// What the epilogue adds: the residual (Fwd), or the output itself (Gx).
+template <typename T, Dense D, int NV>
+__device__ __forceinline__ void load_addend(const ProductArgs &a, int64_t row, int j, float (&r)[8])
+{
+    const int valid = a.ND - j;
+    if constexpr (D == Dense::Fwd) {
+        if (a.res && valid > 0)
+            load_n<NV>(static_cast<const T *>(a.res) + row * a.ldr + j, valid, r);
+    } else {
+        if (a.accumulate && valid > 0)
+            load_n<NV>(static_cast<const T *>(a.out) + row * a.ldo + j, valid, r);
+    }
+}
+
+// The four tiles acc of a 64-column group from column j0 (tile 0's first) of
+// row `row`: epilogue and stores.
+template <typename T, Dense D>
+__device__ __forceinline__ void store_group(const ProductArgs &a, int64_t row, int j0, int q, f32x4 (&acc)[4],
+                                            const float (&add)[sizeof(T) == 4 ? 4 : 2][8])
+{
+    if (row >= a.M)
         return;
-    T *o = static_cast<T *>(a.gx) + r * a.ldgx + k;
-    *o = from_f32<T>(a.accumulate ? to_f32(*o) + acc : acc);
-}
-
-// part[s][k][j] = sum over the rows of split s of x[r][k] d[r][j]; the row
-// k = K holds sum d (the bias gradient)
-template <typename T>
-__global__ void __launch_bounds__(256) linear_gw_kernel(const LinearVjpArgs a, const int nsplit)
-{
-    __shared__ float xs[16][17], ds[16][17];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int k = blockIdx.x * 16 + ty, j = blockIdx.y * 16 + tx, s = blockIdx.z;
-    const int64_t r0 = a.M * s / nsplit, r1 = a.M * (s + 1) / nsplit;
-    const T *x = static_cast<const T *>(a.x);
-    float acc = 0.f;
-    for (int64_t r = r0; r < r1; r += 16) {
-        const int kk = blockIdx.x * 16 + tx;
-        const bool ok = r + ty < r1;
-        xs[ty][tx] = !ok || kk > a.K ? 0.f : kk == a.K ? 1.f : x ? to_f32(x[(r + ty) * a.ldx + kk]) : 0.f;
-        ds[ty][tx] = ok && j < a.N ? slope_grad<T>(a, r + ty, j) : 0.f;
-        __syncthreads();
-        for (int i = 0; i < 16; ++i)
-            acc = __builtin_fmaf(xs[i][ty], ds[i][tx], acc);
-        __syncthreads();
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            float v[8] = {acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
+            store_cols<T, D, 4>(a, row, j0 + col_of_quarter<T>(t, q), v, add[t]);
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            float v[8] = {acc[2 * t][0],     acc[2 * t][1],     acc[2 * t][2],     acc[2 * t][3],
+                          acc[2 * t + 1][0], acc[2 * t + 1][1], acc[2 * t + 1][2], acc[2 * t + 1][3]};
+            store_cols<T, D, 8>(a, row, j0 + col_of_quarter<T>(2 * t, q), v, add[t]);
+        }
     }
-    if (k <= a.K && j < a.N)
-        static_cast<float *>(a.ws)[(static_cast<int64_t>(s) * (a.K + 1) + k) * a.N + j] = acc;
 }
 
-__global__ void __launch_bounds__(256) sum_parts_kernel(const int64_t count, const int n, const int64_t stride,
-                                                        const float *__restrict__ part, float *__restrict__ out,
+template <typename T, Dense D>
+__device__ __forceinline__ void load_group_addend(const ProductArgs &a, int64_t row, int j0, int q,
+                                                  float (&add)[sizeof(T) == 4 ? 4 : 2][8])
+{
+    const int64_t rc = row < a.M ? row : a.M - 1;
+#pragma unroll
+    for (int t = 0; t < (sizeof(T) == 4 ? 4 : 2); ++t)
+        load_addend<T, D, sizeof(T) == 4 ? 4 : 8>(a, rc, j0 + col_of_quarter<T>(sizeof(T) == 4 ? t : 2 * t, q),
+                                                  add[t]);
+}
+
+// Contraction of at most 128: the workgroup keeps its columns of the matrix
+// (nb, a multiple of 64) in LDS and its waves walk 16-row tiles, each on its
+// own, without another barrier. The column blocks of a row range run side by
+// side on one XCD (workgroups b and b + 8 share one), so that the rows are
+// read from memory once.
+template <typename T, Dense D, int KC>
+__global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs a, const int nb, const int nsplit)
+{
+    constexpr int P = kParts<T>;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    auto frag = reinterpret_cast<bf16x8 *>(smem);  // [KC][nb / 16][P][64]
+    float *bias = reinterpret_cast<float *>(smem + static_cast<size_t>(KC) * (nb / 16) * P * 1024);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
+    const int c = lane & 15, q = lane >> 4;
+    const int b8 = blockIdx.x >> 3, s = b8 % nsplit;
+    const int64_t stream = static_cast<int64_t>(b8 / nsplit) * 8 + (blockIdx.x & 7);
+    const int64_t nstream = gridDim.x / nsplit, ntile = (a.M + 15) / 16;
+    if (stream * waves >= ntile)
+        return;  // the whole workgroup: padding of the last group of 8
+    const int n0 = s * nb, ntl = nb / 16;
+    for (int i = threadIdx.x; i < KC * 4 * nb; i += blockDim.x) {
+        // threads along the columns (Fwd) or along k (Gx): the matrix's rows
+        const int col = D == Dense::Fwd ? i % nb : (i / (4 * KC)) % nb;
+        const int kq = D == Dense::Fwd ? i / nb : i % (4 * KC);
+        MatrixChunk<T, D> m;
+        m.load(a, 8 * kq, n0 + col);
+        const Frag<P> f = m.frag();
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            frag[(((kq >> 2) * ntl + tile_of_col<T>(col)) * P + p) * 64 + (kq & 3) * 16 + entry_of_col<T>(col)] =
+                f.p[p];
+    }
+    for (int i = threadIdx.x; i < nb; i += blockDim.x)
+        bias[i] = a.bias && n0 + i < a.ND ? a.bias[n0 + i] : 0.f;
+    __syncthreads();
+
+    RowChunk<T, D> next[KC];
+    auto fetch = [&](int64_t tile) {
+        const int64_t row = tile * 16 + c, rc = row < a.M ? row : a.M - 1;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc)
+            next[kc].load(a, rc, 32 * kc + 8 * q);
+    };
+    int64_t tile = stream * waves + wave;
+    if (tile < ntile)
+        fetch(tile);
+    for (; tile < ntile; tile += nstream * waves) {
+        Frag<kRowParts<T, D>> xf[KC];
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc)
+            xf[kc] = next[kc].frag(a);
+        if (tile + nstream * waves < ntile)
+            fetch(tile + nstream * waves);
+        const int64_t row = tile * 16 + c;
+        for (int g = 0; g < nb / 64 && n0 + 64 * g < a.ND; ++g) {
+            float add[sizeof(T) == 4 ? 4 : 2][8];
+            load_group_addend<T, D>(a, row, n0 + 64 * g, q, add);
+            f32x4 acc[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                acc[t] = *reinterpret_cast<const f32x4 *>(bias + 64 * g + col_of_quarter<T>(t, q));
+#pragma unroll
+            for (int kc = 0; kc < KC; ++kc)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    Frag<P> w;
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        w.p[p] = frag[((kc * ntl + 4 * g + t) * P + p) * 64 + lane];
+                    acc[t] = mma(w, xf[kc], acc[t]);
+                }
+            store_group<T, D>(a, row, n0 + 64 * g, q, acc, add);
+        }
+    }
+}
+
+// Longer contractions: a workgroup of four waves owns 64 RT rows and 128
+// columns; the matrix goes through LDS in chunks of 32 SUB of the contraction
+// (double-buffered, one barrier a chunk), the rows through registers. RT = 2
+// halves the LDS reads and the staging per row; RT = 1 is for grids that
+// would leave compute units without work.
+template <typename T, Dense D, int RT>
+__global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a, const int ncol)
+{
+    constexpr int P = kParts<T>, SUB = sizeof(T) == 4 ? 1 : 2, NT = 8, kCols = 128;
+    constexpr int kItems = SUB * 4 * kCols / 256;  // staged column pieces per thread and chunk
+    __shared__ bf16x8 frag[2][SUB][NT][P][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    // the column blocks of a row block run side by side on one XCD
+    const int b8 = blockIdx.x >> 3;
+    const int64_t rb = static_cast<int64_t>(b8 / ncol) * 8 + (blockIdx.x & 7);
+    const int64_t row0 = (rb * 4 + wave) * 16 * RT;
+    if (rb * 64 * RT >= a.M)
+        return;  // the whole workgroup
+    const int n0 = (b8 % ncol) * kCols;
+
+    f32x4 acc[RT][NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int j = n0 + col_of_quarter<T>(t, q);
+        f32x4 b = {0.f, 0.f, 0.f, 0.f};
+        if (D == Dense::Fwd && a.bias) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[i] = j + i < a.ND ? a.bias[j + i] : 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+            acc[r][t] = b;
+    }
+    const int nk = (a.KD + 32 * SUB - 1) / (32 * SUB);
+    RowChunk<T, D> xn[RT][SUB];
+    MatrixChunk<T, D> wn[kItems];
+    auto item = [&](int n, int &col, int &kq) {
+        const int i = threadIdx.x + 256 * n;
+        col = D == Dense::Fwd ? i % kCols : i / (4 * SUB);
+        kq = D == Dense::Fwd ? i / kCols : i % (4 * SUB);
+    };
+    auto fetch = [&](int it) {
+#pragma unroll
+        for (int n = 0; n < kItems; ++n) {
+            int col, kq;
+            item(n, col, kq);
+            wn[n].load(a, it * 32 * SUB + 8 * kq, n0 + col);
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const int64_t row = row0 + 16 * r + c, rc = row < a.M ? row : a.M - 1;
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+                xn[r][u].load(a, rc, it * 32 * SUB + 32 * u + 8 * q);
+        }
+    };
+    fetch(0);
+    for (int it = 0; it < nk; ++it) {
+        const int buf = it & 1;
+#pragma unroll
+        for (int n = 0; n < kItems; ++n) {
+            int col, kq;
+            item(n, col, kq);
+            const Frag<P> f = wn[n].frag();
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                frag[buf][kq >> 2][tile_of_col<T>(col)][p][(kq & 3) * 16 + entry_of_col<T>(col)] = f.p[p];
+        }
+        Frag<kRowParts<T, D>> xf[RT][SUB];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+                xf[r][u] = xn[r][u].frag(a);
+        // one barrier a chunk: the stores above are seen by every wave, and
+        // the buffer written next was last read before it
+        __syncthreads();
+        if (it + 1 < nk)
+            fetch(it + 1);
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                Frag<P> w;
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    w.p[p] = frag[buf][u][t][p][lane];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    acc[r][t] = mma(w, xf[r][u], acc[r][t]);
+            }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            if (n0 + 64 * g >= a.ND)
+                break;
+            const int64_t row = row0 + 16 * r + c;
+            float add[sizeof(T) == 4 ? 4 : 2][8];
+            load_group_addend<T, D>(a, row, n0 + 64 * g, q, add);
+            f32x4 v[4] = {acc[r][4 * g], acc[r][4 * g + 1], acc[r][4 * g + 2], acc[r][4 * g + 3]};
+            store_group<T, D>(a, row, n0 + 64 * g, q, v, add);
+        }
+}
+
+// Few rows and a long contraction: a workgroup owns 16 rows and 64 columns,
+// its four waves take every fourth chunk of the contraction straight from
+// memory (nothing of the matrix is shared within the workgroup), and the
+// partial tiles are added in wave order through LDS.
+template <typename T, Dense D>
+__global__ void __launch_bounds__(256) product_thin_kernel(const ProductArgs a, const int ncol)
+{
+    __shared__ f32x4 part[3][4][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int n0 = (blockIdx.x % ncol) * 64;
+    const int64_t row = static_cast<int64_t>(blockIdx.x / ncol) * 16 + c, rc = row < a.M ? row : a.M - 1;
+    f32x4 acc[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 32 * wave; k < a.KD; k += 128) {
+        RowChunk<T, D> x;
+        x.load(a, rc, k + 8 * q);
+        MatrixChunk<T, D> w[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)  // this lane's column of tile t: the one whose entry is c
+            w[t].load(a, k + 8 * q, n0 + (sizeof(T) == 4 ? 16 * t + c
+                                                         : 32 * (t >> 1) + 8 * (c >> 2) + 4 * (t & 1) + (c & 3)));
+        const auto xf = x.frag(a);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            acc[t] = mma(w[t].frag(), xf, acc[t]);
+    }
+    if (wave > 0) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            part[wave - 1][t][lane] = acc[t];
+    }
+    __syncthreads();
+    if (wave > 0)
+        return;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int w = 0; w < 3; ++w)
+            acc[t] += part[w][t][lane];
+        const int j = n0 + col_of_quarter<T>(t, q);
+        if (D == Dense::Fwd && a.bias) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[t][i] += j + i < a.ND ? a.bias[j + i] : 0.f;
+        }
+    }
+    float add[sizeof(T) == 4 ? 4 : 2][8];
+    load_group_addend<T, D>(a, row, n0, q, add);
+    store_group<T, D>(a, row, n0, q, acc, add);
+}
+
+constexpr int kComputeUnits = 256;
+
+// Dynamic LDS beyond the runtime's default limit of 64 KiB has to be asked
+// for, once per kernel.
+template <typename T, Dense D, int KC>
+static hipError_t launch_resident(const ProductArgs &a, dim3 grid, dim3 block, size_t lds, int nb, int nsplit,
+                                  hipStream_t stream)
+{
+    if (lds > 64 * 1024) {
+        static const hipError_t e = hipFuncSetAttribute(
+            reinterpret_cast<const void *>(&product_resident_kernel<T, D, KC>),
+            hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        if (e != hipSuccess)
+            return e;
+    }
+    hipLaunchKernelGGL((product_resident_kernel<T, D, KC>), grid, block, lds, stream, a, nb, nsplit);
+    return hipGetLastError();
+}
+
+template <typename T, Dense D>
+static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
+{
+    const int64_t ntile = (a.M + 15) / 16;
+    if (a.KD <= 128) {
+        const int kc = (a.KD + 31) / 32;
+        const int nb = a.ND <= 64 ? 64 : 128, nsplit = (a.ND + nb - 1) / nb;
+        const size_t lds = static_cast<size_t>(kc) * (nb / 16) * kParts<T> * 1024 + nb * sizeof(float);
+        const int waves = lds <= 40 * 1024 ? 4 : 8;
+        const int per_cu = static_cast<int>(160 * 1024 / lds) < 16 / waves ? static_cast<int>(160 * 1024 / lds)
+                                                                            : 16 / waves;
+        int64_t streams = (ntile + waves - 1) / waves;
+        const int64_t most = (static_cast<int64_t>(kComputeUnits) * per_cu + nsplit - 1) / nsplit;
+        streams = ((streams < most ? streams : most) + 7) / 8 * 8;
+        const dim3 grid(static_cast<unsigned>(streams * nsplit)), block(64 * waves);
+        switch (kc) {
+        case 1: return launch_resident<T, D, 1>(a, grid, block, lds, nb, nsplit, stream);
+        case 2: return launch_resident<T, D, 2>(a, grid, block, lds, nb, nsplit, stream);
+        case 3: return launch_resident<T, D, 3>(a, grid, block, lds, nb, nsplit, stream);
+        default: return launch_resident<T, D, 4>(a, grid, block, lds, nb, nsplit, stream);
+        }
+    }
+    const int ncol = (a.ND + 127) / 128;
+    const int64_t wide = (a.M + 127) / 128 * ncol, half = (a.M + 63) / 64 * ncol;
+    if (half < kComputeUnits) {
+        const int nc = (a.ND + 63) / 64;
+        hipLaunchKernelGGL((product_thin_kernel<T, D>), dim3(static_cast<unsigned>(ntile * nc)), dim3(256), 0, stream,
+                           a, nc);
+    } else if (wide < 2 * kComputeUnits) {
+        hipLaunchKernelGGL((product_stream_kernel<T, D, 1>),
+                           dim3(static_cast<unsigned>(((a.M + 63) / 64 + 7) / 8 * 8 * ncol)), dim3(256), 0, stream, a,
+                           ncol);
+    } else {
+        hipLaunchKernelGGL((product_stream_kernel<T, D, 2>),
+                           dim3(static_cast<unsigned>(((a.M + 127) / 128 + 7) / 8 * 8 * ncol)), dim3(256), 0, stream,
+                           a, ncol);
+    }
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// The VJP over panels of 64 rows. A workgroup walks its panels: d and x are
+// formed in registers from one read of gy, z and x, cut into bf16 parts and
+// put into LDS row by row; then
+//   gx = d W^T: the contraction runs along a row, so fragments of d are read
+//     from LDS as they lie, and each wave keeps its columns of W in registers
+//     for all panels;
+//   gW += x^T d: the contraction runs along the rows; the transposing LDS
+//     read (ds_read_b64_tr_b16) hands a lane four rows of one column, and the
+//     result stays in the accumulators until the last panel.
+// So each input is read once and only gx and one partial gW per workgroup are
+// written (added by sum_parts_kernel in a fixed order). gb is summed in
+// registers from d itself. With K and N above 128 the same kernel forms a 128
+// x 128 block of gW per workgroup (no gx) from d made once by slope_kernel.
+//
+// Row r of a fragment's eight: the transposing read of half t takes rows 16 t
+// + 4 q .. + 3 of a 32-row step (x and d alike, the order within the
+// contraction being free), and rows are padded by 32 bytes, so that the eight
+// rows that half a wave reads lie on distinct banks.
+
+struct PanelArgs {
+    LinearVjpArgs v;
+    const float *d;   // d [M][N], or null: from gy and z
+    int64_t npanel;
+    int nsplit;       // workgroups along the panels
+    int nkb;          // blocks of 32 KC along K (1 with gx)
+};
+
+constexpr int kPanel = 64;
+
+template <typename T, int KC, int NC>
+struct PanelShape {
+    static constexpr int PX = kParts<T>;
+    static constexpr int W = KC == 4 || NC == 4 ? 8 : 4;      // waves
+    static constexpr int SX = 32 * KC + 16, SD = 32 * NC + 16;  // row strides (elements)
+    static constexpr int lds = 2 * kPanel * (PX * SX + 3 * SD);
+};
+
+__device__ __forceinline__ bf16x8 read_transposed(const bf16bits *rows, int stride, int step, int col0, int lane)
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 *lds4;
+    const int q = lane >> 4, l = lane & 15;
+    const bf16bits *p = rows + (32 * step + 4 * q + (l >> 2)) * stride + col0 + 4 * (l & 3);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 16 * stride));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <typename T, int KC, int NC, bool FromD>
+__global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(const PanelArgs p)
+{
+    using S = PanelShape<T, KC, NC>;
+    constexpr int PX = S::PX, W = S::W, SX = S::SX, SD = S::SD;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    bf16bits *dl = reinterpret_cast<bf16bits *>(smem);    // [3][64][SD]
+    bf16bits *xl = dl + 3 * kPanel * SD;                  // [PX][64][SX]
+    const LinearVjpArgs &a = p.v;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int s = blockIdx.x % p.nsplit, blk = blockIdx.x / p.nsplit;
+    const int k0 = (blk % p.nkb) * 32 * KC, j0 = (blk / p.nkb) * 32 * NC;
+    const int K = a.K, N = a.N;
+    const bool want_gx = a.gx != nullptr, want_gw = a.gW != nullptr, want_gb = a.gb != nullptr && k0 == 0;
+
+    // loads: wave w takes rows 16 (w % 4) .. + 15 of the panel, and with eight
+    // waves every other chunk of 32 columns
+    constexpr int WS = W / 4, NL = (NC + WS - 1) / WS, KL = (KC + WS - 1) / WS;
+    const int lrow = 16 * (wave & 3) + c, ch0 = wave >> 2;
+    Raw8<std::conditional_t<FromD, float, T>> gn[NL];
+    Raw8<T> zn[NL], xn[KL];
+    auto fetch = [&](int64_t panel) {
+        const int64_t r = panel * kPanel + lrow, rc = r < a.M ? r : a.M - 1;
+#pragma unroll
+        for (int n = 0; n < NL; ++n) {
+            const int j = j0 + 32 * (ch0 + WS * n) + 8 * q;
+            if (NC % WS && ch0 + WS * n >= NC)
+                continue;
+            const int valid = N - j;
+            if constexpr (FromD) {
+                gn[n].load(p.d + rc * N + j, valid);
+            } else {
+                gn[n].load(static_cast<const T *>(a.gy) + rc * a.ldgy + j, valid);
+                if (a.act != kActNone)
+                    zn[n].load(static_cast<const T *>(a.z) + rc * a.ldz + j, valid);
+            }
+        }
+        if (want_gw) {
+#pragma unroll
+            for (int n = 0; n < KL; ++n) {
+                const int k = k0 + 32 * (ch0 + WS * n) + 8 * q;
+                if (KC % WS && ch0 + WS * n >= KC)
+                    continue;
+                xn[n].load(static_cast<const T *>(a.x) + rc * a.ldx + k, K - k);
+            }
+        }
+    };
+
+    // gx: a wave owns G column tiles (a pair for bf16, whose lanes store eight
+    // columns) and 4 / RS of the four row tiles
+    constexpr int G = sizeof(T) == 4 ? 1 : 2, groups = 2 * KC / G, RS0 = W / groups, RS = RS0 < 4 ? RS0 : 4;
+    constexpr int RT = 4 / RS;
+    const int grp = wave % groups, rt0 = (wave / groups) * RT;
+    const bool gx_wave = want_gx && wave / groups < RS;
+    Frag<PX> wf[G][NC];
+    if (gx_wave) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                const int k = sizeof(T) == 4 ? 16 * grp + c : 32 * grp + 8 * (c >> 2) + 4 * g + (c & 3);
+                const int j = 32 * n + 8 * q;
+                Raw8<T> raw;
+                raw.load(static_cast<const T *>(a.W) + static_cast<int64_t>(k < K ? k : 0) * N + j,
+                         k < K ? N - j : 0);
+                wf[g][n] = raw.template frag<PX>();
+            }
+    }
+
+    // gW: waves as WK x WN, each KT x JT tiles of 16 x 16
+    constexpr int WN = W == 4 || NC == 1 ? 2 : 4, WK = W / WN, KT = 2 * KC / WK, JT = 2 * NC / WN;
+    const int kt0 = (wave / WN) * KT, jt0 = (wave % WN) * JT;
+    f32x4 acc[KT][JT];
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float gb[NL][8];
+#pragma unroll
+    for (int n = 0; n < NL; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            gb[n][i] = 0.f;
+
+    if (s < p.npanel)
+        fetch(s);
+    for (int64_t panel = s; panel < p.npanel; panel += p.nsplit) {
+        const bool live = panel * kPanel + lrow < a.M;
+#pragma unroll
+        for (int n = 0; n < NL; ++n) {
+            const int ch = ch0 + WS * n;
+            if (NC % WS && ch >= NC)
+                continue;
+            float d[8];
+            gn[n].get(d);
+            if constexpr (!FromD) {
+                if (a.act != kActNone) {
+                    float z[8];
+                    zn[n].get(z);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        d[i] *= act_slope(a.act, z[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d[i] = live ? d[i] : 0.f;
+                gb[n][i] += d[i];
+            }
+            const Frag<3> f = split8<3>(d);
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+                *reinterpret_cast<bf16x8 *>(dl + (t * kPanel + lrow) * SD + 32 * ch + 8 * q) = f.p[t];
+        }
+        if (want_gw) {
+#pragma unroll
+            for (int n = 0; n < KL; ++n) {
+                const int ch = ch0 + WS * n;
+                if (KC % WS && ch >= KC)
+                    continue;
+                const Frag<PX> f = xn[n].template frag<PX>();
+#pragma unroll
+                for (int t = 0; t < PX; ++t)
+                    *reinterpret_cast<bf16x8 *>(xl + (t * kPanel + lrow) * SX + 32 * ch + 8 * q) = f.p[t];
+            }
+        }
+        if (panel + p.nsplit < p.npanel)
+            fetch(panel + p.nsplit);
+        __syncthreads();
+        if (gx_wave) {
+            constexpr int PD = sizeof(T) == 4 ? 3 : 2;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                f32x4 o[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    o[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int n = 0; n < NC; ++n) {
+                    Frag<PD> df;
+#pragma unroll
+                    for (int t = 0; t < PD; ++t)
+                        df.p[t] = *reinterpret_cast<const bf16x8 *>(
+                            dl + (t * kPanel + 16 * (rt0 + r) + c) * SD + 32 * n + 8 * q);
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        o[g] = mma(wf[g][n], df, o[g]);
+                }
+                const int64_t row = panel * kPanel + 16 * (rt0 + r) + c;
+                const int k = sizeof(T) == 4 ? 16 * grp + 4 * q : 32 * grp + 8 * q;
+                if (row < a.M && k < K) {
+                    T *dst = static_cast<T *>(a.gx) + row * a.ldgx + k;
+                    float v[8];
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[4 * g + i] = o[g][i];
+                    if (a.accumulate) {
+                        float was[8];
+                        load_n<4 * G>(dst, K - k, was);
+#pragma unroll
+                        for (int i = 0; i < 4 * G; ++i)
+                            v[i] += was[i];
+                    }
+                    store_n<4 * G>(dst, K - k, v);
+                }
+            }
+        }
+        if (want_gw) {
+#pragma unroll
+            for (int st = 0; st < kPanel / 32; ++st) {
+                Frag<3> df[JT];
+#pragma unroll
+                for (int j = 0; j < JT; ++j)
+#pragma unroll
+                    for (int t = 0; t < 3; ++t)
+                        df[j].p[t] = read_transposed(dl + t * kPanel * SD, SD, st, 16 * (jt0 + j), lane);
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    Frag<PX> xf;
+#pragma unroll
+                    for (int t = 0; t < PX; ++t)
+                        xf.p[t] = read_transposed(xl + t * kPanel * SX, SX, st, 16 * (kt0 + i), lane);
+#pragma unroll
+                    for (int j = 0; j < JT; ++j)
+                        acc[i][j] = mma(xf, df[j], acc[i][j]);
+                }
+            }
+        }
+        __syncthreads();  // the next panel overwrites the rows
+    }
+
+    float *part = static_cast<float *>(a.ws) + static_cast<int64_t>(s) * (static_cast<int64_t>(K) + 1) * N;
+    if (want_gw) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int j = 0; j < JT; ++j) {
+                const int jj = j0 + 16 * (jt0 + j) + c;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int k = k0 + 16 * (kt0 + i) + 4 * q + r;
+                    if (k < K && jj < N)
+                        part[static_cast<int64_t>(k) * N + jj] = acc[i][j][r];
+                }
+            }
+    }
+    if (want_gb) {
+        // over the 16 rows of the lanes, then the four row tiles through LDS
+        float *sums = reinterpret_cast<float *>(smem);  // [4][32 NC]
+#pragma unroll
+        for (int n = 0; n < NL; ++n) {
+            const int ch = ch0 + WS * n;
+            if (NC % WS && ch >= NC)
+                continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float v = gb[n][i];
+#pragma unroll
+                for (int m = 1; m < 16; m <<= 1)
+                    v += __shfl_xor(v, m);
+                if (c == 0)
+                    sums[(wave & 3) * 32 * NC + 32 * ch + 8 * q + i] = v;
+            }
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < 32 * NC; j += 64 * W)
+            if (j0 + j < N)
+                part[static_cast<int64_t>(K) * N + j0 + j] =
+                    (sums[j] + sums[32 * NC + j]) + (sums[2 * 32 * NC + j] + sums[3 * 32 * NC + j]);
+    }
+}
+
+// d = gy act'(z) in float, dense rows
+template <typename T>
+__global__ void __launch_bounds__(256) slope_kernel(const LinearVjpArgs a, float *__restrict__ d)
+{
+    const int nv = (a.N + 7) / 8;
+    const int64_t count = a.M * nv;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
+        const int64_t r = i / nv;
+        const int j = static_cast<int>(i - r * nv) * 8;
+        float g[8], z[8];
+        load8(static_cast<const T *>(a.gy) + r * a.ldgy + j, a.N - j, g);
+        load8(static_cast<const T *>(a.z) + r * a.ldz + j, a.N - j, z);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            g[k] *= act_slope(a.act, z[k]);
+        store8(d + r * a.N + j, a.N - j, g);
+    }
+}
+
+// out0, out1 (+)= the sums over n sets of n0 + n1 partial values: 16 columns
+// of 16 threads a workgroup; a thread adds every 16th set in order, then the
+// 16 sums are added as a tree (chains of n / 16 keep a long sum's rounding
+// down, and spread its reads).
+__global__ void __launch_bounds__(256) sum_parts_kernel(const int64_t n0, float *out0, const int64_t n1, float *out1,
+                                                        const int n, const float *__restrict__ part,
                                                         const int accumulate)
 {
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
-        float v = 0.f;
-        for (int s = 0; s < n; ++s)
-            v += part[s * stride + i];
-        out[i] = accumulate ? out[i] + v : v;
+    __shared__ float lds[16][17];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int64_t count = n0 + n1, i = blockIdx.x * 16ll + tx;
+    float v = 0.f;
+    if (i < count)
+        for (int s = ty; s < n; s += 16)
+            v += part[s * count + i];
+    lds[ty][tx] = v;
+    for (int d = 8; d; d >>= 1) {
+        __syncthreads();
+        if (ty < d)
+            lds[ty][tx] += lds[ty + d][tx];
     }
+    if (ty > 0 || i >= count)
+        return;
+    float *o = i < n0 ? out0 : out1;
+    if (!o)
+        return;
+    o += i < n0 ? i : i - n0;
+    *o = accumulate ? *o + lds[0][tx] : lds[0][tx];
 }
 
-hipError_t launch_sum_parts(int64_t count, int n, int64_t stride, const float *part, float *out, bool accumulate,
-                            hipStream_t stream)
+hipError_t launch_sum_parts(int64_t n0, float *out0, int64_t n1, float *out1, int n, const float *part,
+                            bool accumulate, hipStream_t stream)
 {
-    const int64_t blocks = (count + 255) / 256;
-    hipLaunchKernelGGL(sum_parts_kernel, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
-                       stream, count, n, stride, part, out, accumulate ? 1 : 0);
+    hipLaunchKernelGGL(sum_parts_kernel, dim3(static_cast<unsigned>((n0 + n1 + 15) / 16)), dim3(256), 0, stream, n0,
+                       out0, n1, out1, n, part, accumulate ? 1 : 0);
     return hipGetLastError();
 }
 
@@ -116,55 +874,127 @@ hipError_t launch_linear(const LinearArgs &a, hipStream_t stream)
 {
     if (a.M == 0)
         return hipSuccess;
-    const dim3 grid(static_cast<unsigned>((a.M + 15) / 16), static_cast<unsigned>((a.N + 15) / 16));
-    if (a.bf16)
-        hipLaunchKernelGGL(linear_kernel<bf16bits>, grid, dim3(256), 0, stream, a);
-    else
-        hipLaunchKernelGGL(linear_kernel<float>, grid, dim3(256), 0, stream, a);
+    const ProductArgs p{a.M, a.K, a.N, a.x, a.ldx, nullptr, 0, a.W, a.bias, a.act, a.res, a.ldr,
+                        a.y, a.ldy, a.z, a.ldz, false};
+    return a.bf16 ? launch_product<bf16bits, Dense::Fwd>(p, stream) : launch_product<float, Dense::Fwd>(p, stream);
+}
+
+// How a VJP call is cut: all in one panel kernel where K and N are at most
+// 128, else d once, gx as a product and gW in blocks.
+struct VjpCut {
+    bool fused;
+    int kc, nc;          // chunks of 32 of a block: 1, 2 or 4
+    int nkb, nnb;        // blocks along K and N
+    int64_t npanel;
+    int nsplit;          // panel streams, and partial sets
+    size_t d_bytes, part_bytes;
+};
+
+static VjpCut vjp_cut(int64_t M, int K, int N, bool bf16)
+{
+    VjpCut v{};
+    auto chunks = [](int n) { return n <= 32 ? 1 : n <= 64 ? 2 : 4; };
+    v.kc = chunks(K);
+    v.nc = chunks(N);
+    v.nkb = (K + 127) / 128;
+    v.nnb = (N + 127) / 128;
+    v.fused = K <= 128 && N <= 128;
+    v.npanel = (M + kPanel - 1) / kPanel;
+    const int lds = 2 * kPanel * ((bf16 ? 1 : 3) * (32 * v.kc + 16) + 3 * (32 * v.nc + 16));
+    const int waves = v.kc == 4 || v.nc == 4 ? 8 : 4;
+    const int per_cu = 160 * 1024 / lds < 16 / waves ? 160 * 1024 / lds : 16 / waves;
+    const int64_t blocks = static_cast<int64_t>(v.nkb) * v.nnb;
+    int64_t s = (static_cast<int64_t>(kComputeUnits) * per_cu + blocks - 1) / blocks;
+    s = s < v.npanel ? s : v.npanel;
+    v.nsplit = static_cast<int>(s < 1 ? 1 : s);
+    v.d_bytes = v.fused ? 0 : (sizeof(float) * static_cast<size_t>(M) * N + 15) / 16 * 16;
+    v.part_bytes = sizeof(float) * static_cast<size_t>(v.nsplit) * (static_cast<size_t>(K) + 1) * N;
+    return v;
+}
+
+size_t linear_vjp_workspace_bytes(int64_t M, int K, int N, bool bf16)
+{
+    if (M == 0)
+        return 0;
+    const VjpCut v = vjp_cut(M, K, N, bf16);
+    return v.d_bytes + v.part_bytes;
+}
+
+template <typename T, int KC, int NC, bool FromD>
+static hipError_t launch_panel(const PanelArgs &p, int blocks, hipStream_t stream)
+{
+    using S = PanelShape<T, KC, NC>;
+    if (S::lds > 64 * 1024) {
+        static const hipError_t e =
+            hipFuncSetAttribute(reinterpret_cast<const void *>(&panel_kernel<T, KC, NC, FromD>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, S::lds);
+        if (e != hipSuccess)
+            return e;
+    }
+    hipLaunchKernelGGL((panel_kernel<T, KC, NC, FromD>), dim3(static_cast<unsigned>(p.nsplit * blocks)),
+                       dim3(64 * S::W), S::lds, stream, p);
     return hipGetLastError();
 }
 
-// Splits of the rows for the weight gradient: enough workgroups to fill the
-// chip, at least 64 rows each.
-static int gw_splits(int64_t M, int K, int N)
+template <typename T>
+static hipError_t panel_by_shape(const PanelArgs &p, const VjpCut &v, hipStream_t stream)
 {
-    const int64_t tiles = static_cast<int64_t>((K + 1 + 15) / 16) * ((N + 15) / 16);
-    int64_t s = (2048 + tiles - 1) / tiles;
-    s = s < M / 64 ? s : M / 64;
-    return static_cast<int>(s < 1 ? 1 : s > 256 ? 256 : s);
+    if (!v.fused)
+        return p.d ? launch_panel<T, 4, 4, true>(p, v.nkb * v.nnb, stream)
+                   : launch_panel<T, 4, 4, false>(p, v.nkb * v.nnb, stream);
+    switch (v.kc * 8 + v.nc) {
+    case 9: return launch_panel<T, 1, 1, false>(p, 1, stream);
+    case 10: return launch_panel<T, 1, 2, false>(p, 1, stream);
+    case 12: return launch_panel<T, 1, 4, false>(p, 1, stream);
+    case 17: return launch_panel<T, 2, 1, false>(p, 1, stream);
+    case 18: return launch_panel<T, 2, 2, false>(p, 1, stream);
+    case 20: return launch_panel<T, 2, 4, false>(p, 1, stream);
+    case 33: return launch_panel<T, 4, 1, false>(p, 1, stream);
+    case 34: return launch_panel<T, 4, 2, false>(p, 1, stream);
+    default: return launch_panel<T, 4, 4, false>(p, 1, stream);
+    }
 }
 
-size_t linear_vjp_workspace_bytes(int64_t M, int K, int N, bool)
+template <typename T>
+static hipError_t linear_vjp(const LinearVjpArgs &a, hipStream_t stream)
 {
-    return M == 0 ? 0 : sizeof(float) * static_cast<size_t>(gw_splits(M, K, N)) * (K + 1) * static_cast<size_t>(N);
+    const bool sums = a.gW || a.gb;
+    const VjpCut v = vjp_cut(a.M, a.K, a.N, a.bf16);
+    PanelArgs p{a, nullptr, v.npanel, v.nsplit, v.nkb};
+    hipError_t e = hipSuccess;
+    if (!v.fused || !sums) {
+        // without the sums there is no workspace either: d as the product goes
+        if (sums && a.act != kActNone) {
+            float *d = reinterpret_cast<float *>(static_cast<unsigned char *>(a.ws) + v.part_bytes);
+            const int64_t blocks = (a.M * ((a.N + 7) / 8) + 255) / 256;
+            hipLaunchKernelGGL(slope_kernel<T>, dim3(static_cast<unsigned>(blocks < 16384 ? blocks : 16384)),
+                               dim3(256), 0, stream, a, d);
+            if ((e = hipGetLastError()) != hipSuccess)
+                return e;
+            p.d = d;
+        }
+        if (a.gx) {
+            const ProductArgs g{a.M, a.N, a.K, p.d ? p.d : a.gy, p.d ? a.N : a.ldgy, a.z, a.ldz, a.W, nullptr, a.act,
+                                nullptr, 0, a.gx, a.ldgx, nullptr, 0, a.accumulate};
+            e = p.d ? launch_product<T, Dense::GxD>(g, stream) : launch_product<T, Dense::Gx>(g, stream);
+        }
+        p.v.gx = nullptr;
+    }
+    return e == hipSuccess && sums ? panel_by_shape<T>(p, v, stream) : e;
 }
 
 hipError_t launch_linear_vjp(const LinearVjpArgs &a, hipStream_t stream)
 {
-    const int64_t kn = static_cast<int64_t>(a.K) * a.N;
-    if (a.M > 0 && a.gx) {
-        const dim3 grid(static_cast<unsigned>((a.M + 15) / 16), static_cast<unsigned>((a.K + 15) / 16));
-        if (a.bf16)
-            hipLaunchKernelGGL(linear_gx_kernel<bf16bits>, grid, dim3(256), 0, stream, a);
-        else
-            hipLaunchKernelGGL(linear_gx_kernel<float>, grid, dim3(256), 0, stream, a);
+    const bool sums = a.gW || a.gb;
+    hipError_t e = hipSuccess;
+    int nsplit = 0;
+    if (a.M > 0) {
+        nsplit = vjp_cut(a.M, a.K, a.N, a.bf16).nsplit;
+        e = a.bf16 ? linear_vjp<bf16bits>(a, stream) : linear_vjp<float>(a, stream);
     }
-    if (!a.gW && !a.gb)
-        return hipGetLastError();
-    const int S = a.M == 0 ? 0 : gw_splits(a.M, a.K, a.N);
-    if (S > 0) {
-        const dim3 grid(static_cast<unsigned>((a.K + 1 + 15) / 16), static_cast<unsigned>((a.N + 15) / 16), S);
-        if (a.bf16)
-            hipLaunchKernelGGL(linear_gw_kernel<bf16bits>, grid, dim3(256), 0, stream, a, S);
-        else
-            hipLaunchKernelGGL(linear_gw_kernel<float>, grid, dim3(256), 0, stream, a, S);
-    }
-    const float *part = static_cast<const float *>(a.ws);
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && a.gW)
-        e = launch_sum_parts(kn, S, kn + a.N, part, a.gW, a.accumulate, stream);
-    if (e == hipSuccess && a.gb)
-        e = launch_sum_parts(a.N, S, kn + a.N, part ? part + kn : nullptr, a.gb, a.accumulate, stream);
+    if (e == hipSuccess && sums)
+        e = launch_sum_parts(static_cast<int64_t>(a.K) * a.N, a.gW, a.N, a.gb, nsplit,
+                             static_cast<const float *>(a.ws), a.accumulate, stream);
     return e;
 }
 
