@@ -61,6 +61,40 @@ __device__ __forceinline__ Frag<P> split8(const float (&v)[8])
     return f;
 }
 
+// The same with rounded instead of truncated parts (nearest even): the dropped
+// products are smaller and of either sign, at the same cost, but values above
+// the largest bf16 (3.39e38) would become infinite.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t rounded_pair(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+}
+__device__ __forceinline__ uint32_t take_pair(float &a, float &b)
+{
+    const uint32_t u = rounded_pair(a, b);
+    a -= __uint_as_float(u << 16);
+    b -= __uint_as_float(u & 0xFFFF0000u);
+    return u;
+}
+template <int P>
+__device__ __forceinline__ Frag<P> split8_rounded(const float (&v)[8])
+{
+    Frag<P> f;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w[i] = v[i];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        u32x4 u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            u[i] = take_pair(w[2 * i], w[2 * i + 1]);
+        f.p[p] = __builtin_bit_cast(bf16x8, u);
+    }
+    return f;
+}
+
 // Eight consecutive stored values, the ones from `valid` on zero (not read).
 __device__ __forceinline__ void load8(const float *p, int valid, float (&v)[8])
 {
@@ -202,18 +236,51 @@ __device__ __forceinline__ void store_n(T *p, int valid, const float (&v)[8])
     }
 }
 
-// acc += the products of parts i of a and j of b with i + j <= 2, the
-// smallest first.
+// acc[k] += the products of parts i of a[k] and j of b up to order i + j =
+// most parts - 1 (three parts: six products; two: three; one against P: P),
+// the smallest first, over all k before the next, so that instructions that
+// follow each other do not wait for each other's result.
+template <int PA, int PB, int N>
+__device__ __forceinline__ void mma(const Frag<PA> (&a)[N], const Frag<PB> &b, f32x4 (&acc)[N])
+{
+#pragma unroll
+    for (int s = (PA > PB ? PA : PB) - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < PA; ++i)
+            if (s - i >= 0 && s - i < PB) {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[k].p[i], b.p[s - i], acc[k], 0, 0, 0);
+            }
+}
+
 template <int PA, int PB>
 __device__ __forceinline__ f32x4 mma(const Frag<PA> &a, const Frag<PB> &b, f32x4 acc)
 {
 #pragma unroll
-    for (int s = (PA + PB - 2 < 2 ? PA + PB - 2 : 2); s >= 0; --s)
+    for (int s = (PA > PB ? PA : PB) - 1; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < PA; ++i)
             if (s - i >= 0 && s - i < PB)
                 acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], acc, 0, 0, 0);
     return acc;
+}
+
+// Fragment of a contraction that runs along the rows of a row-major bf16
+// matrix in LDS, rows 32 step .. + 31, columns col0 .. + 15: the transposing
+// read hands a lane four rows of its column. Slots 0 .. 3 of quarter q are rows
+// 4 q .. + 3 of the step, slots 4 .. 7 the rows 16 below (both operands alike:
+// the order within a contraction is free). With rows of 32 bytes more than a
+// multiple of 64 the eight rows that half a wave reads lie on distinct banks.
+__device__ __forceinline__ bf16x8 read_transposed(const bf16bits *rows, int stride, int step, int col0, int lane)
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 *lds4;
+    const int q = lane >> 4, l = lane & 15;
+    const bf16bits *p = rows + (32 * step + 4 * q + (l >> 2)) * stride + col0 + 4 * (l & 3);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 16 * stride));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 }  // namespace etp

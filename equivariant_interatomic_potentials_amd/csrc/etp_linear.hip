@@ -543,11 +543,6 @@ static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
 // registers from d itself. With K and N above 128 the same kernel forms a 128
 // x 128 block of gW per workgroup (no gx) from d made once by slope_kernel.
 //
-// Row r of a fragment's eight: the transposing read of half t takes rows 16 t
-// + 4 q .. + 3 of a 32-row step (x and d alike, the order within the
-// contraction being free), and rows are padded by 32 bytes, so that the eight
-// rows that half a wave reads lie on distinct banks.
-
 struct PanelArgs {
     LinearVjpArgs v;
     const float *d;   // d [M][N], or null: from gy and z
@@ -565,17 +560,6 @@ struct PanelShape {
     static constexpr int SX = 32 * KC + 16, SD = 32 * NC + 16;  // row strides (elements)
     static constexpr int lds = 2 * kPanel * (PX * SX + 3 * SD);
 };
-
-__device__ __forceinline__ bf16x8 read_transposed(const bf16bits *rows, int stride, int step, int col0, int lane)
-{
-    typedef short s16x4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) s16x4 *lds4;
-    const int q = lane >> 4, l = lane & 15;
-    const bf16bits *p = rows + (32 * step + 4 * q + (l >> 2)) * stride + col0 + 4 * (l & 3);
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 16 * stride));
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
-}
 
 template <typename T, int KC, int NC, bool FromD>
 __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(const PanelArgs p)
