@@ -43,12 +43,37 @@ __device__ __forceinline__ float logistic(float z)
 
 constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
 
+// The normal distribution function and density. With x = |z| / sqrt 2, the
+// tail is Phi(-|z|) = exp(-x^2) u(t), t = 1 / (1 + 0.4 x), u the polynomial
+// t (c0 + c1 t + ... + c7 t^7) fitted by least squares (reweighted towards the
+// smallest largest error) to exp(x^2) erfc(x) / 2 on [0, 9]: 3e-10 of Phi
+// everywhere, 8e-6 of the tail out to |z| = 6. A third of the cost of a
+// library erf, which would bound the bf16 forward by its arithmetic.
+__device__ __forceinline__ float normal_cdf(float z, float &density)
+{
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.4f * 0.707106781f, fabsf(z), 1.f));
+    const float e = __builtin_amdgcn_exp2f(-0.721347520f * z * z);
+    float p = 0.0387523736f;
+    p = __builtin_fmaf(p, t, -0.204188902f);
+    p = __builtin_fmaf(p, t, 0.354209376f);
+    p = __builtin_fmaf(p, t, -0.197550078f);
+    p = __builtin_fmaf(p, t, 0.209061794f);
+    p = __builtin_fmaf(p, t, 0.0691124589f);
+    p = __builtin_fmaf(p, t, 0.118083984f);
+    p = __builtin_fmaf(p, t, 0.112518994f);
+    const float tail = p * t * e;
+    density = 0.398942280f * e;
+    return z > 0.f ? 1.f - tail : tail;
+}
+
 __device__ __forceinline__ float act_value(int act, float z)
 {
     if (act == kActSilu)
         return z * logistic(z);
-    if (act == kActGelu)
-        return 0.5f * z * (1.f + erff(z * 0.707106781f));
+    if (act == kActGelu) {
+        float density;
+        return z * normal_cdf(z, density);
+    }
     return z;
 }
 
@@ -58,8 +83,11 @@ __device__ __forceinline__ float act_slope(int act, float z)
         const float s = logistic(z);
         return s * __builtin_fmaf(z, 1.f - s, 1.f);
     }
-    if (act == kActGelu)
-        return __builtin_fmaf(z * 0.398942280f, expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.707106781f)));
+    if (act == kActGelu) {
+        float density;
+        const float cdf = normal_cdf(z, density);
+        return __builtin_fmaf(z, density, cdf);
+    }
     return 1.f;
 }
 

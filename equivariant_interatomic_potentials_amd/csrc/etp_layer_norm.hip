@@ -54,10 +54,14 @@ __device__ __forceinline__ float group_sum(float v)
         v = dpp_add<0x141>(v);  // row_half_mirror
     if constexpr (N >= 16)
         v = dpp_add<0x140>(v);  // row_mirror
-    if constexpr (N >= 32)
-        v += __shfl_xor(v, 16);
-    if constexpr (N >= 64)
-        v += __shfl_xor(v, 32);
+    if constexpr (N >= 32) {  // rows of 16 lanes with their neighbours, then the wave's halves
+        const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+    }
+    if constexpr (N >= 64) {
+        const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+    }
     return v;
 }
 
@@ -104,9 +108,18 @@ struct Columns {
                     row[col[n] + i] = from_f32<T>(v[i]);
         }
     }
-    __device__ __forceinline__ float weight(const float *w, int n, int i, float none) const
+    // the columns' entries of a weight vector, `none` where there is no vector
+    __device__ __forceinline__ void weights(const float *w, int n, float none, float (&v)[kVec<T>]) const
     {
-        return w && own(n, i) ? w[col[n] + i] : none;
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            u[i] = none;
+        if (w)
+            load_n<kVec<T>>(w + col[n], hi, u);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i)
+            v[i] = u[i];
     }
 };
 
@@ -118,12 +131,10 @@ __global__ void __launch_bounds__(256) layer_norm_kernel(const NormArgs a)
     const Columns<T, LPR, NI, RAG> cs(lane % LPR, a.C);
     float gamma[NI][V], beta[NI][V];
 #pragma unroll
-    for (int n = 0; n < NI; ++n)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            gamma[n][i] = cs.weight(a.gamma, n, i, 1.f);
-            beta[n][i] = cs.weight(a.beta, n, i, 0.f);
-        }
+    for (int n = 0; n < NI; ++n) {
+        cs.weights(a.gamma, n, 1.f, gamma[n]);
+        cs.weights(a.beta, n, 0.f, beta[n]);
+    }
     const float inv = 1.f / static_cast<float>(a.C);
     const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * RPW;
     int64_t r = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * RPW + lane / LPR;
@@ -180,27 +191,29 @@ __global__ void __launch_bounds__(256) layer_norm_kernel(const NormArgs a)
     }
 }
 
+constexpr int kVjpWaves = 8;
+
 // Input gradient and this workgroup's column sums, part[b][0][c] = sum gy h,
 // part[b][1][c] = sum gy over its rows: lanes, then the wave's row groups,
-// then the four waves, in a fixed order.
+// then the waves in turn.
 template <typename T, int LPR, int NI, bool RAG>
-__global__ void __launch_bounds__(256) layer_norm_vjp_kernel(const NormVjpArgs a)
+__global__ void __launch_bounds__(64 * kVjpWaves) layer_norm_vjp_kernel(const NormVjpArgs a)
 {
     constexpr int V = kVec<T>, RPW = 64 / LPR;
-    __shared__ float sums[4][2][LPR * NI * V];
+    __shared__ float sums[2][LPR * NI * V];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const Columns<T, LPR, NI, RAG> cs(lane % LPR, a.C);
     float gamma[NI][V], gg[NI][V], gb[NI][V];
 #pragma unroll
-    for (int n = 0; n < NI; ++n)
+    for (int n = 0; n < NI; ++n) {
+        cs.weights(a.gamma, n, 1.f, gamma[n]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            gamma[n][i] = cs.weight(a.gamma, n, i, 1.f);
+        for (int i = 0; i < V; ++i)
             gg[n][i] = gb[n][i] = 0.f;
-        }
+    }
     const float inv = 1.f / static_cast<float>(a.C);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * RPW;
-    int64_t r = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * RPW + lane / LPR;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kVjpWaves * RPW;
+    int64_t r = (static_cast<int64_t>(blockIdx.x) * kVjpWaves + wave) * RPW + lane / LPR;
     RawVec<T> nx[NI], ng[NI];
     float nmean, nrstd;
     auto fetch = [&](int64_t row) {
@@ -268,25 +281,32 @@ __global__ void __launch_bounds__(256) layer_norm_vjp_kernel(const NormVjpArgs a
     for (int n = 0; n < NI; ++n)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float u = gg[n][i], w = gb[n][i];
 #pragma unroll
             for (int m = LPR; m < 64; m <<= 1) {
-                u += __shfl_xor(u, m);
-                w += __shfl_xor(w, m);
-            }
-            if (lane < LPR) {
-                sums[wave][0][(n * LPR + lane) * V + i] = u;
-                sums[wave][1][(n * LPR + lane) * V + i] = w;
+                gg[n][i] += __shfl_xor(gg[n][i], m);
+                gb[n][i] += __shfl_xor(gb[n][i], m);
             }
         }
-    __syncthreads();
+    for (int w = 0; w < kVjpWaves; ++w) {
+        if (wave == w && lane < LPR) {
+#pragma unroll
+            for (int n = 0; n < NI; ++n)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int e = (n * V + i) * LPR + lane;
+                    sums[0][e] = w ? sums[0][e] + gg[n][i] : gg[n][i];
+                    sums[1][e] = w ? sums[1][e] + gb[n][i] : gb[n][i];
+                }
+        }
+        __syncthreads();
+    }
     float *part = static_cast<float *>(a.ws) + static_cast<int64_t>(blockIdx.x) * 2 * a.C;
-    for (int k = threadIdx.x; k < 2 * LPR * NI * V; k += 256) {
-        const int w = k >= LPR * NI * V, e = k - w * LPR * NI * V;
-        const int want = e / V * V, last = a.C > V ? a.C - V : 0;
-        const int c = (RAG && want > last ? last : want) + e % V;  // the vector's column (Columns)
+    for (int k = threadIdx.x; k < 2 * LPR * NI * V; k += 64 * kVjpWaves) {
+        const int w = k >= LPR * NI * V, e = k - w * LPR * NI * V;  // e: column order
+        const int vec = e / V, i = e % V, want = vec * V, last = a.C > V ? a.C - V : 0;
+        const int c = (RAG && want > last ? last : want) + i;  // the vector's column (Columns)
         if (c >= want && c < a.C)
-            part[w * a.C + c] = (sums[0][w][e] + sums[1][w][e]) + (sums[2][w][e] + sums[3][w][e]);
+            part[w * a.C + c] = sums[w][(vec / LPR * V + i) * LPR + vec % LPR];
     }
 }
 
@@ -382,15 +402,38 @@ __global__ void __launch_bounds__(256) layer_norm_long_gw_kernel(const NormVjpAr
 
 constexpr int kLongRow = 2048;
 
-// Calls f<LPR, NI, RAG>() for rows of C <= 2048 columns in vectors of V.
-template <int V, typename F>
-static hipError_t by_columns(int C, F &&f)
+// How rows of C <= 2048 columns lie in a wave: lanes per row and vectors per
+// lane. Several rows a wave and sums within 16 lanes come first; the forward
+// holds up to 32 columns a lane, the VJP, which needs six registers a column,
+// 16 where the row allows it.
+struct NormShape {
+    int lpr, ni;
+};
+
+static NormShape norm_shape(int C, int V, bool vjp)
 {
-    const int vecs = (C + V - 1) / V;
-#define ETP_NORM_CASE(L, N)                                                                      \
-    if (vecs <= L * N)                                                                           \
+    const int vecs = (C + V - 1) / V, most = vjp && V == 8 ? 2 : 4;
+    int lpr = 1;
+    while (lpr < 16 && lpr < vecs)
+        lpr *= 2;
+    int ni = 1;
+    while (ni < most && lpr * ni < vecs)
+        ni *= 2;
+    while (lpr < 64 && lpr * ni < vecs)
+        lpr *= 2;
+    while (lpr * ni < vecs)
+        ni *= 2;
+    return {lpr, ni};
+}
+
+// Calls f(LPR, NI, RAG) for the shape s of rows of C columns in vectors of V.
+template <int V, typename F>
+static hipError_t by_shape(NormShape s, int C, F &&f)
+{
+#define ETP_NORM_CASE(L, N)                                                                       \
+    if (s.lpr == L && s.ni == N)                                                                  \
         return C == L * N * V ? f(std::integral_constant<int, L>{}, std::integral_constant<int, N>{}, \
-                                  std::false_type{})                                             \
+                                  std::false_type{})                                              \
                               : f(std::integral_constant<int, L>{}, std::integral_constant<int, N>{}, \
                                   std::true_type{});
     ETP_NORM_CASE(1, 1)
@@ -398,8 +441,10 @@ static hipError_t by_columns(int C, F &&f)
     ETP_NORM_CASE(4, 1)
     ETP_NORM_CASE(8, 1)
     ETP_NORM_CASE(16, 1)
-    ETP_NORM_CASE(32, 1)
-    ETP_NORM_CASE(64, 1)
+    ETP_NORM_CASE(16, 2)
+    ETP_NORM_CASE(16, 4)
+    ETP_NORM_CASE(32, 2)
+    ETP_NORM_CASE(32, 4)
     ETP_NORM_CASE(64, 2)
     ETP_NORM_CASE(64, 4)
     if constexpr (V == 4) {
@@ -409,10 +454,15 @@ static hipError_t by_columns(int C, F &&f)
     return hipErrorInvalidValue;
 }
 
-// Workgroups of four waves over M rows of which a wave takes rpw at a time.
+// Workgroups of `waves` waves over M rows, of which a wave takes rpw at a time.
+static int64_t norm_blocks(int64_t M, int rpw, int waves)
+{
+    return (M + static_cast<int64_t>(waves) * rpw - 1) / (static_cast<int64_t>(waves) * rpw);
+}
+
 static unsigned norm_grid(int64_t M, int rpw, int most)
 {
-    const int64_t b = (M + 4 * rpw - 1) / (4 * rpw);
+    const int64_t b = norm_blocks(M, rpw, 4);
     return static_cast<unsigned>(b < most ? b : most);
 }
 
@@ -423,8 +473,8 @@ static hipError_t norm_forward(const NormArgs &a, hipStream_t stream)
         hipLaunchKernelGGL(layer_norm_long_kernel<T>, dim3(norm_grid(a.M, 1, 2048)), dim3(256), 0, stream, a);
         return hipGetLastError();
     }
-    return by_columns<kVec<T>>(a.C, [&](auto l, auto n, auto rag) {
-        hipLaunchKernelGGL((layer_norm_kernel<T, l(), n(), rag()>), dim3(norm_grid(a.M, 64 / l(), 2048)), dim3(256), 0,
+    return by_shape<kVec<T>>(norm_shape(a.C, kVec<T>, false), a.C, [&](auto l, auto n, auto rag) {
+        hipLaunchKernelGGL((layer_norm_kernel<T, l(), n(), rag()>), dim3(norm_grid(a.M, 64 / l(), 1024)), dim3(256), 0,
                            stream, a);
         return hipGetLastError();
     });
@@ -437,18 +487,22 @@ hipError_t launch_layer_norm(const NormArgs &a, hipStream_t stream)
     return a.bf16 ? norm_forward<bf16bits>(a, stream) : norm_forward<float>(a, stream);
 }
 
-// Partial column sums of the VJP: one set per workgroup.
+// Partial column sums of the VJP: one set per workgroup, as many workgroups
+// as the registers let run at once (two a compute unit up to eight columns a
+// lane: 66 us against 70 with four, 75 with one, on 441172 x 64 floats; one
+// beyond: 16 us against 22 with more, on 5184 x 777 bf16), all with the same
+// number of turns.
 static int norm_parts(int64_t M, int C, bool bf16)
 {
     if (C > kLongRow) {
         const int64_t s = M / 16;
         return static_cast<int>(s < 1 ? 1 : s > 512 ? 512 : s);
     }
-    const int V = bf16 ? 8 : 4, vecs = (C + V - 1) / V;
-    int lpr = 1;
-    while (lpr < 64 && lpr < vecs)
-        lpr *= 2;
-    return static_cast<int>(norm_grid(M, 64 / lpr, 1024));
+    const int V = bf16 ? 8 : 4;
+    const NormShape s = norm_shape(C, V, true);
+    const int64_t blocks = norm_blocks(M, 64 / s.lpr, kVjpWaves), most = s.ni * V <= 8 ? 512 : 256;
+    const int64_t turns = (blocks + most - 1) / most;
+    return static_cast<int>((blocks + turns - 1) / turns);
 }
 
 size_t layer_norm_vjp_workspace_bytes(int64_t M, int C, bool bf16)
@@ -467,9 +521,9 @@ static hipError_t norm_vjp(const NormVjpArgs &a, int S, hipStream_t stream)
                                dim3(256), 0, stream, a, S);
         return hipGetLastError();
     }
-    return by_columns<kVec<T>>(a.C, [&](auto l, auto n, auto rag) {
-        hipLaunchKernelGGL((layer_norm_vjp_kernel<T, l(), n(), rag()>), dim3(static_cast<unsigned>(S)), dim3(256), 0,
-                           stream, a);
+    return by_shape<kVec<T>>(norm_shape(a.C, kVec<T>, true), a.C, [&](auto l, auto n, auto rag) {
+        hipLaunchKernelGGL((layer_norm_vjp_kernel<T, l(), n(), rag()>), dim3(static_cast<unsigned>(S)),
+                           dim3(64 * kVjpWaves), 0, stream, a);
         return hipGetLastError();
     });
 }

@@ -117,10 +117,77 @@ __device__ __forceinline__ int col_of_quarter(int t, int q)
     return sizeof(T) == 4 ? 16 * t + 4 * q : 32 * (t >> 1) + 8 * q + 4 * (t & 1);
 }
 
-// Entries k .. k + 7 of column j of the [KD][ND] matrix as loaded, zero
-// outside, and as matrix-core parts.
+// The matrix in LDS, in chunks of 32 of the contraction by nb columns, parts
+// apart. Forward: W's rows run along the columns, so it lies row by row as in
+// memory (16-byte loads and stores) and the transposing read hands a lane its
+// eight k of a column; LDS row 4 q + i (16 + 4 q + i) of a chunk holds k = 8 q +
+// i (8 q + 4 + i), the slots that read takes, and the columns of a pair of
+// tiles are interleaved as the result wants them. Input gradient: W's rows run
+// along the contraction and lie in fragment order.
 template <typename T, Dense D>
-struct MatrixChunk {
+struct MatrixLds {
+    static constexpr int P = kParts<T>;
+    static constexpr bool kRows = D == Dense::Fwd;
+    // elements of one chunk of nb columns
+    static __host__ __device__ constexpr int chunk(int nb) { return kRows ? P * 32 * (nb + 16) : P * 32 * nb; }
+    // pieces of eight elements of one chunk
+    static __host__ __device__ constexpr int pieces(int nb) { return 4 * nb; }
+
+    // piece i of the chunk from k0: consecutive threads along W's rows
+    static __device__ __forceinline__ void load(const ProductArgs &a, int i, int nb, int k0, int n0, Raw8<T> &v)
+    {
+        const T *W = static_cast<const T *>(a.W);
+        int row, col, valid;
+        if constexpr (kRows) {
+            row = k0 + i / (nb / 8);
+            col = n0 + i % (nb / 8) * 8;
+            valid = row < a.KD ? a.ND - col : 0;
+        } else {
+            row = n0 + i / 4;
+            col = k0 + i % 4 * 8;
+            valid = row < a.ND ? a.KD - col : 0;
+        }
+        v.load(W + (valid > 0 ? static_cast<int64_t>(row) * (kRows ? a.ND : a.KD) + col : 0), valid);
+    }
+    static __device__ __forceinline__ void store(bf16bits *m, int i, int nb, const Raw8<T> &v)
+    {
+        const Frag<P> f = v.template frag<P>();
+        if constexpr (kRows) {
+            const int k = i / (nb / 8), j = i % (nb / 8) * 8, r = 16 * ((k >> 2) & 1) + 4 * (k >> 3) + (k & 3);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                bf16bits *at = m + (p * 32 + r) * (nb + 16);
+                if constexpr (sizeof(T) == 4) {
+                    *reinterpret_cast<bf16x8 *>(at + j) = f.p[p];
+                } else {  // columns 32 g + 8 q .. + 3 and .. + 7: entries 4 q .. + 3 of tiles 2 g and 2 g + 1
+                    const u32x4 u = __builtin_bit_cast(u32x4, f.p[p]);
+                    at += (j & ~31) + ((j & 31) >> 1);
+                    *reinterpret_cast<uint2 *>(at) = uint2{u[0], u[1]};
+                    *reinterpret_cast<uint2 *>(at + 16) = uint2{u[2], u[3]};
+                }
+            }
+        } else {
+            const int j = i / 4, q = i % 4;
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                *reinterpret_cast<bf16x8 *>(
+                    m + ((tile_of_col<T>(j) * P + p) * 64 + q * 16 + entry_of_col<T>(j)) * 8) = f.p[p];
+        }
+    }
+    static __device__ __forceinline__ Frag<P> tile(const bf16bits *m, int t, int nb, int lane)
+    {
+        Frag<P> f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            f.p[p] = kRows ? read_transposed(m + p * 32 * (nb + 16), nb + 16, 0, 16 * t, lane)
+                           : *reinterpret_cast<const bf16x8 *>(m + ((t * P + p) * 64 + lane) * 8);
+        return f;
+    }
+};
+
+// A lane's eight k of one column straight from memory.
+template <typename T, Dense D>
+struct MatrixColumn {
     T v[8];
     __device__ __forceinline__ void load(const ProductArgs &a, int k, int j)
     {
@@ -238,10 +305,10 @@ __device__ __forceinline__ void load_group_addend(const ProductArgs &a, int64_t 
 template <typename T, Dense D, int KC>
 __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs a, const int nb, const int nsplit)
 {
-    constexpr int P = kParts<T>;
+    using Mx = MatrixLds<T, D>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    auto frag = reinterpret_cast<bf16x8 *>(smem);  // [KC][nb / 16][P][64]
-    float *bias = reinterpret_cast<float *>(smem + static_cast<size_t>(KC) * (nb / 16) * P * 1024);
+    bf16bits *matrix = reinterpret_cast<bf16bits *>(smem);  // [KC] chunks
+    float *bias = reinterpret_cast<float *>(matrix + KC * Mx::chunk(nb));
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
     const int c = lane & 15, q = lane >> 4;
@@ -250,18 +317,12 @@ __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs
     const int64_t nstream = gridDim.x / nsplit, ntile = (a.M + 15) / 16;
     if (stream * waves >= ntile)
         return;  // the whole workgroup: padding of the last group of 8
-    const int n0 = s * nb, ntl = nb / 16;
-    for (int i = threadIdx.x; i < KC * 4 * nb; i += blockDim.x) {
-        // threads along the columns (Fwd) or along k (Gx): the matrix's rows
-        const int col = D == Dense::Fwd ? i % nb : (i / (4 * KC)) % nb;
-        const int kq = D == Dense::Fwd ? i / nb : i % (4 * KC);
-        MatrixChunk<T, D> m;
-        m.load(a, 8 * kq, n0 + col);
-        const Frag<P> f = m.frag();
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-            frag[(((kq >> 2) * ntl + tile_of_col<T>(col)) * P + p) * 64 + (kq & 3) * 16 + entry_of_col<T>(col)] =
-                f.p[p];
+    const int n0 = s * nb;
+    for (int i = threadIdx.x; i < KC * Mx::pieces(nb); i += blockDim.x) {
+        const int kc = i / Mx::pieces(nb), j = i % Mx::pieces(nb);
+        Raw8<T> v;
+        Mx::load(a, j, nb, 32 * kc, n0, v);
+        Mx::store(matrix + kc * Mx::chunk(nb), j, nb, v);
     }
     for (int i = threadIdx.x; i < nb; i += blockDim.x)
         bias[i] = a.bias && n0 + i < a.ND ? a.bias[n0 + i] : 0.f;
@@ -295,13 +356,8 @@ __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs
 #pragma unroll
             for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    Frag<P> w;
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        w.p[p] = frag[((kc * ntl + 4 * g + t) * P + p) * 64 + lane];
-                    acc[t] = mma(w, xf[kc], acc[t]);
-                }
+                for (int t = 0; t < 4; ++t)
+                    acc[t] = mma(Mx::tile(matrix + kc * Mx::chunk(nb), 4 * g + t, nb, lane), xf[kc], acc[t]);
             store_group<T, D>(a, row, n0 + 64 * g, q, acc, add);
         }
     }
@@ -315,9 +371,10 @@ __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs
 template <typename T, Dense D, int RT>
 __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a, const int ncol)
 {
-    constexpr int P = kParts<T>, SUB = sizeof(T) == 4 ? 1 : 2, NT = 8, kCols = 128;
-    constexpr int kItems = SUB * 4 * kCols / 256;  // staged column pieces per thread and chunk
-    __shared__ bf16x8 frag[2][SUB][NT][P][64];
+    using Mx = MatrixLds<T, D>;
+    constexpr int SUB = sizeof(T) == 4 ? 1 : 2, NT = 8, kCols = 128;
+    constexpr int kItems = Mx::pieces(kCols) / 256;  // per thread and chunk of 32
+    __shared__ __attribute__((aligned(16))) bf16bits matrix[2][SUB][Mx::chunk(kCols)];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
     // the column blocks of a row block run side by side on one XCD
@@ -344,19 +401,13 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
     }
     const int nk = (a.KD + 32 * SUB - 1) / (32 * SUB);
     RowChunk<T, D> xn[RT][SUB];
-    MatrixChunk<T, D> wn[kItems];
-    auto item = [&](int n, int &col, int &kq) {
-        const int i = threadIdx.x + 256 * n;
-        col = D == Dense::Fwd ? i % kCols : i / (4 * SUB);
-        kq = D == Dense::Fwd ? i / kCols : i % (4 * SUB);
-    };
+    Raw8<T> wn[SUB][kItems];
     auto fetch = [&](int it) {
 #pragma unroll
-        for (int n = 0; n < kItems; ++n) {
-            int col, kq;
-            item(n, col, kq);
-            wn[n].load(a, it * 32 * SUB + 8 * kq, n0 + col);
-        }
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int n = 0; n < kItems; ++n)
+                Mx::load(a, threadIdx.x + 256 * n, kCols, (it * SUB + u) * 32, n0, wn[u][n]);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const int64_t row = row0 + 16 * r + c, rc = row < a.M ? row : a.M - 1;
@@ -369,14 +420,10 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
     for (int it = 0; it < nk; ++it) {
         const int buf = it & 1;
 #pragma unroll
-        for (int n = 0; n < kItems; ++n) {
-            int col, kq;
-            item(n, col, kq);
-            const Frag<P> f = wn[n].frag();
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-                frag[buf][kq >> 2][tile_of_col<T>(col)][p][(kq & 3) * 16 + entry_of_col<T>(col)] = f.p[p];
-        }
+            for (int n = 0; n < kItems; ++n)
+                Mx::store(matrix[buf][u], threadIdx.x + 256 * n, kCols, wn[u][n]);
         Frag<kRowParts<T, D>> xf[RT][SUB];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -392,10 +439,7 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                Frag<P> w;
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                    w.p[p] = frag[buf][u][t][p][lane];
+                const auto w = Mx::tile(matrix[buf][u], t, kCols, lane);
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
                     acc[r][t] = mma(w, xf[r][u], acc[r][t]);
@@ -434,7 +478,7 @@ __global__ void __launch_bounds__(256) product_thin_kernel(const ProductArgs a, 
     for (int k = 32 * wave; k < a.KD; k += 128) {
         RowChunk<T, D> x;
         x.load(a, rc, k + 8 * q);
-        MatrixChunk<T, D> w[4];
+        MatrixColumn<T, D> w[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)  // this lane's column of tile t: the one whose entry is c
             w[t].load(a, k + 8 * q, n0 + (sizeof(T) == 4 ? 16 * t + c
@@ -495,7 +539,7 @@ static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
     if (a.KD <= 128) {
         const int kc = (a.KD + 31) / 32;
         const int nb = a.ND <= 64 ? 64 : 128, nsplit = (a.ND + nb - 1) / nb;
-        const size_t lds = static_cast<size_t>(kc) * (nb / 16) * kParts<T> * 1024 + nb * sizeof(float);
+        const size_t lds = sizeof(bf16bits) * kc * MatrixLds<T, D>::chunk(nb) + nb * sizeof(float);
         const int waves = lds <= 40 * 1024 ? 4 : 8;
         const int per_cu = static_cast<int>(160 * 1024 / lds) < 16 / waves ? static_cast<int>(160 * 1024 / lds)
                                                                             : 16 / waves;
@@ -529,7 +573,7 @@ static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
 }
 
 // ---------------------------------------------------------------------------
-// The VJP over panels of 64 rows. A workgroup walks its panels: d and x are
+// The VJP over panels of rows. A workgroup walks its panels: d and x are
 // formed in registers from one read of gy, z and x, cut into bf16 parts and
 // put into LDS row by row; then
 //   gx = d W^T: the contraction runs along a row, so fragments of d are read
@@ -551,24 +595,30 @@ struct PanelArgs {
     int nkb;          // blocks of 32 KC along K (1 with gx)
 };
 
-constexpr int kPanel = 64;
-
-template <typename T, int KC, int NC>
+// Two panels' parts lie in LDS: while one feeds the products the next is
+// formed and written (one barrier a panel). A panel has 64 rows, or 32 where
+// two of 64 would take more than 80 KiB (160 KiB with eight waves, of which a
+// compute unit holds one workgroup either way).
 struct PanelShape {
-    static constexpr int PX = kParts<T>;
-    static constexpr int W = KC == 4 || NC == 4 ? 8 : 4;      // waves
-    static constexpr int SX = 32 * KC + 16, SD = 32 * NC + 16;  // row strides (elements)
-    static constexpr int lds = 2 * kPanel * (PX * SX + 3 * SD);
+    int px, waves, sx, sd, rows, lds;  // parts of x, row strides (elements)
+    constexpr PanelShape(bool bf16, int kc, int nc)
+        : px(bf16 ? 1 : 3), waves(kc == 4 || nc == 4 ? 8 : 4), sx(32 * kc + 16), sd(32 * nc + 16),
+          rows(2 * 2 * 64 * (px * sx + 3 * sd) <= (waves == 8 ? 160 : 80) * 1024 ? 64 : 32),
+          lds(2 * 2 * rows * (px * sx + 3 * sd))
+    {
+    }
 };
+template <typename T, int KC, int NC>
+constexpr PanelShape kPanelShape{sizeof(T) == 2, KC, NC};
 
 template <typename T, int KC, int NC, bool FromD>
-__global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(const PanelArgs p)
+__global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves)) panel_kernel(const PanelArgs p)
 {
-    using S = PanelShape<T, KC, NC>;
-    constexpr int PX = S::PX, W = S::W, SX = S::SX, SD = S::SD;
+    constexpr PanelShape S = kPanelShape<T, KC, NC>;
+    constexpr int PX = S.px, W = S.waves, SX = S.sx, SD = S.sd, kRows = S.rows;
+    constexpr int kBuf = kRows * (PX * SX + 3 * SD);  // elements of one panel
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    bf16bits *dl = reinterpret_cast<bf16bits *>(smem);    // [3][64][SD]
-    bf16bits *xl = dl + 3 * kPanel * SD;                  // [PX][64][SX]
+    bf16bits *const lds = reinterpret_cast<bf16bits *>(smem);  // [2] of d [3][kRows][SD], x [PX][kRows][SX]
     const LinearVjpArgs &a = p.v;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
@@ -577,14 +627,14 @@ __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(
     const int K = a.K, N = a.N;
     const bool want_gx = a.gx != nullptr, want_gw = a.gW != nullptr, want_gb = a.gb != nullptr && k0 == 0;
 
-    // loads: wave w takes rows 16 (w % 4) .. + 15 of the panel, and with eight
-    // waves every other chunk of 32 columns
-    constexpr int WS = W / 4, NL = (NC + WS - 1) / WS, KL = (KC + WS - 1) / WS;
-    const int lrow = 16 * (wave & 3) + c, ch0 = wave >> 2;
+    // loads: wave w takes 16 rows of the panel and every WS-th chunk of 32
+    // columns
+    constexpr int kTiles = kRows / 16, WS = W / kTiles, NL = (NC + WS - 1) / WS, KL = (KC + WS - 1) / WS;
+    const int lrow = 16 * (wave % kTiles) + c, ch0 = wave / kTiles;
     Raw8<std::conditional_t<FromD, float, T>> gn[NL];
     Raw8<T> zn[NL], xn[KL];
     auto fetch = [&](int64_t panel) {
-        const int64_t r = panel * kPanel + lrow, rc = r < a.M ? r : a.M - 1;
+        const int64_t r = panel * kRows + lrow, rc = r < a.M ? r : a.M - 1;
 #pragma unroll
         for (int n = 0; n < NL; ++n) {
             const int j = j0 + 32 * (ch0 + WS * n) + 8 * q;
@@ -611,9 +661,9 @@ __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(
     };
 
     // gx: a wave owns G column tiles (a pair for bf16, whose lanes store eight
-    // columns) and 4 / RS of the four row tiles
-    constexpr int G = sizeof(T) == 4 ? 1 : 2, groups = 2 * KC / G, RS0 = W / groups, RS = RS0 < 4 ? RS0 : 4;
-    constexpr int RT = 4 / RS;
+    // columns) and RT of the row tiles
+    constexpr int G = sizeof(T) == 4 ? 1 : 2, groups = 2 * KC / G, RS0 = W / groups, RS = RS0 < kTiles ? RS0 : kTiles;
+    constexpr int RT = kTiles / RS;
     const int grp = wave % groups, rt0 = (wave / groups) * RT;
     const bool gx_wave = want_gx && wave / groups < RS;
     Frag<PX> wf[G][NC];
@@ -647,10 +697,10 @@ __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(
         for (int i = 0; i < 8; ++i)
             gb[n][i] = 0.f;
 
-    if (s < p.npanel)
-        fetch(s);
-    for (int64_t panel = s; panel < p.npanel; panel += p.nsplit) {
-        const bool live = panel * kPanel + lrow < a.M;
+    // the fetched panel's parts into LDS
+    auto put = [&](int64_t panel, bf16bits *dl) __attribute__((always_inline)) {
+        bf16bits *xl = dl + 3 * kRows * SD;
+        const bool live = panel * kRows + lrow < a.M;
 #pragma unroll
         for (int n = 0; n < NL; ++n) {
             const int ch = ch0 + WS * n;
@@ -675,7 +725,7 @@ __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(
             const Frag<3> f = split8<3>(d);
 #pragma unroll
             for (int t = 0; t < 3; ++t)
-                *reinterpret_cast<bf16x8 *>(dl + (t * kPanel + lrow) * SD + 32 * ch + 8 * q) = f.p[t];
+                *reinterpret_cast<bf16x8 *>(dl + (t * kRows + lrow) * SD + 32 * ch + 8 * q) = f.p[t];
         }
         if (want_gw) {
 #pragma unroll
@@ -686,12 +736,28 @@ __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(
                 const Frag<PX> f = xn[n].template frag<PX>();
 #pragma unroll
                 for (int t = 0; t < PX; ++t)
-                    *reinterpret_cast<bf16x8 *>(xl + (t * kPanel + lrow) * SX + 32 * ch + 8 * q) = f.p[t];
+                    *reinterpret_cast<bf16x8 *>(xl + (t * kRows + lrow) * SX + 32 * ch + 8 * q) = f.p[t];
             }
         }
-        if (panel + p.nsplit < p.npanel)
-            fetch(panel + p.nsplit);
+    };
+
+    if (s < p.npanel) {
+        fetch(s);
+        put(s, lds);
+        if (s + p.nsplit < p.npanel)
+            fetch(s + p.nsplit);
+    }
+    int buf = 0;
+    for (int64_t panel = s; panel < p.npanel; panel += p.nsplit, buf ^= 1) {
+        // one barrier a panel: the panel's parts are seen by every wave, and
+        // the buffer written next was last read before it
         __syncthreads();
+        const bf16bits *dl = lds + buf * kBuf, *xl = dl + 3 * kRows * SD;
+        if (panel + p.nsplit < p.npanel) {
+            put(panel + p.nsplit, lds + (buf ^ 1) * kBuf);
+            if (panel + 2 * p.nsplit < p.npanel)
+                fetch(panel + 2 * p.nsplit);
+        }
         if (gx_wave) {
             constexpr int PD = sizeof(T) == 4 ? 3 : 2;
 #pragma unroll
@@ -706,12 +772,12 @@ __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(
 #pragma unroll
                     for (int t = 0; t < PD; ++t)
                         df.p[t] = *reinterpret_cast<const bf16x8 *>(
-                            dl + (t * kPanel + 16 * (rt0 + r) + c) * SD + 32 * n + 8 * q);
+                            dl + (t * kRows + 16 * (rt0 + r) + c) * SD + 32 * n + 8 * q);
 #pragma unroll
                     for (int g = 0; g < G; ++g)
                         o[g] = mma(wf[g][n], df, o[g]);
                 }
-                const int64_t row = panel * kPanel + 16 * (rt0 + r) + c;
+                const int64_t row = panel * kRows + 16 * (rt0 + r) + c;
                 const int k = sizeof(T) == 4 ? 16 * grp + 4 * q : 32 * grp + 8 * q;
                 if (row < a.M && k < K) {
                     T *dst = static_cast<T *>(a.gx) + row * a.ldgx + k;
@@ -734,27 +800,27 @@ __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(
         }
         if (want_gw) {
 #pragma unroll
-            for (int st = 0; st < kPanel / 32; ++st) {
+            for (int st = 0; st < kRows / 32; ++st) {
                 Frag<3> df[JT];
 #pragma unroll
                 for (int j = 0; j < JT; ++j)
 #pragma unroll
                     for (int t = 0; t < 3; ++t)
-                        df[j].p[t] = read_transposed(dl + t * kPanel * SD, SD, st, 16 * (jt0 + j), lane);
+                        df[j].p[t] = read_transposed(dl + t * kRows * SD, SD, st, 16 * (jt0 + j), lane);
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {
                     Frag<PX> xf;
 #pragma unroll
                     for (int t = 0; t < PX; ++t)
-                        xf.p[t] = read_transposed(xl + t * kPanel * SX, SX, st, 16 * (kt0 + i), lane);
+                        xf.p[t] = read_transposed(xl + t * kRows * SX, SX, st, 16 * (kt0 + i), lane);
 #pragma unroll
                     for (int j = 0; j < JT; ++j)
                         acc[i][j] = mma(xf, df[j], acc[i][j]);
                 }
             }
         }
-        __syncthreads();  // the next panel overwrites the rows
     }
+    __syncthreads();  // the sums below reuse the space
 
     float *part = static_cast<float *>(a.ws) + static_cast<int64_t>(s) * (static_cast<int64_t>(K) + 1) * N;
     if (want_gw) {
@@ -772,8 +838,8 @@ __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(
             }
     }
     if (want_gb) {
-        // over the 16 rows of the lanes, then the four row tiles through LDS
-        float *sums = reinterpret_cast<float *>(smem);  // [4][32 NC]
+        // over the 16 rows of the lanes, then the row tiles through LDS
+        float *sums = reinterpret_cast<float *>(smem);  // [kTiles][32 NC]
 #pragma unroll
         for (int n = 0; n < NL; ++n) {
             const int ch = ch0 + WS * n;
@@ -786,14 +852,18 @@ __global__ void __launch_bounds__((64 * PanelShape<T, KC, NC>::W)) panel_kernel(
                 for (int m = 1; m < 16; m <<= 1)
                     v += __shfl_xor(v, m);
                 if (c == 0)
-                    sums[(wave & 3) * 32 * NC + 32 * ch + 8 * q + i] = v;
+                    sums[(wave % kTiles) * 32 * NC + 32 * ch + 8 * q + i] = v;
             }
         }
         __syncthreads();
-        for (int j = threadIdx.x; j < 32 * NC; j += 64 * W)
+        for (int j = threadIdx.x; j < 32 * NC; j += 64 * W) {
+            float v = 0.f;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+                v += sums[t * 32 * NC + j];
             if (j0 + j < N)
-                part[static_cast<int64_t>(K) * N + j0 + j] =
-                    (sums[j] + sums[32 * NC + j]) + (sums[2 * 32 * NC + j] + sums[3 * 32 * NC + j]);
+                part[static_cast<int64_t>(K) * N + j0 + j] = v;
+        }
     }
 }
 
@@ -816,23 +886,33 @@ __global__ void __launch_bounds__(256) slope_kernel(const LinearVjpArgs a, float
     }
 }
 
-// out0, out1 (+)= the sums over n sets of n0 + n1 partial values: 16 columns
-// of 16 threads a workgroup; a thread adds every 16th set in order, then the
-// 16 sums are added as a tree (chains of n / 16 keep a long sum's rounding
-// down, and spread its reads).
-__global__ void __launch_bounds__(256) sum_parts_kernel(const int64_t n0, float *out0, const int64_t n1, float *out1,
-                                                        const int n, const float *__restrict__ part,
-                                                        const int accumulate)
+// out0, out1 (+)= the sums over n sets of n0 + n1 partial values: Cols columns
+// of Ways threads a workgroup; a thread adds every Ways-th set in order, then
+// the Ways sums are added as a tree (short chains keep a long sum's rounding
+// down and its reads in flight together).
+template <int Cols, int Ways>
+__global__ void __launch_bounds__(Cols * Ways) sum_parts_kernel(const int64_t n0, float *out0, const int64_t n1,
+                                                                float *out1, const int n,
+                                                                const float *__restrict__ part, const int accumulate)
 {
-    __shared__ float lds[16][17];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t count = n0 + n1, i = blockIdx.x * 16ll + tx;
+    __shared__ float lds[Ways][Cols + 1];
+    const int tx = threadIdx.x % Cols, ty = threadIdx.x / Cols;
+    const int64_t count = n0 + n1, i = static_cast<int64_t>(blockIdx.x) * Cols + tx;
     float v = 0.f;
-    if (i < count)
-        for (int s = ty; s < n; s += 16)
+    if (i < count) {
+        int s = ty;
+        for (; s + 3 * Ways < n; s += 4 * Ways) {
+            float u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                u[k] = part[(s + k * Ways) * count + i];
+            v += (u[0] + u[1]) + (u[2] + u[3]);
+        }
+        for (; s < n; s += Ways)
             v += part[s * count + i];
+    }
     lds[ty][tx] = v;
-    for (int d = 8; d; d >>= 1) {
+    for (int d = Ways / 2; d; d >>= 1) {
         __syncthreads();
         if (ty < d)
             lds[ty][tx] += lds[ty + d][tx];
@@ -849,8 +929,13 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const int64_t n0, float 
 hipError_t launch_sum_parts(int64_t n0, float *out0, int64_t n1, float *out1, int n, const float *part,
                             bool accumulate, hipStream_t stream)
 {
-    hipLaunchKernelGGL(sum_parts_kernel, dim3(static_cast<unsigned>((n0 + n1 + 15) / 16)), dim3(256), 0, stream, n0,
-                       out0, n1, out1, n, part, accumulate ? 1 : 0);
+    const int64_t count = n0 + n1;
+    if (n > 64)
+        hipLaunchKernelGGL((sum_parts_kernel<16, 64>), dim3(static_cast<unsigned>((count + 15) / 16)), dim3(1024), 0,
+                           stream, n0, out0, n1, out1, n, part, accumulate ? 1 : 0);
+    else
+        hipLaunchKernelGGL((sum_parts_kernel<64, 4>), dim3(static_cast<unsigned>((count + 63) / 64)), dim3(256), 0,
+                           stream, n0, out0, n1, out1, n, part, accumulate ? 1 : 0);
     return hipGetLastError();
 }
 
@@ -883,10 +968,9 @@ static VjpCut vjp_cut(int64_t M, int K, int N, bool bf16)
     v.nkb = (K + 127) / 128;
     v.nnb = (N + 127) / 128;
     v.fused = K <= 128 && N <= 128;
-    v.npanel = (M + kPanel - 1) / kPanel;
-    const int lds = 2 * kPanel * ((bf16 ? 1 : 3) * (32 * v.kc + 16) + 3 * (32 * v.nc + 16));
-    const int waves = v.kc == 4 || v.nc == 4 ? 8 : 4;
-    const int per_cu = 160 * 1024 / lds < 16 / waves ? 160 * 1024 / lds : 16 / waves;
+    const PanelShape shape(bf16, v.fused ? v.kc : 4, v.fused ? v.nc : 4);
+    v.npanel = (M + shape.rows - 1) / shape.rows;
+    const int per_cu = 160 * 1024 / shape.lds < 16 / shape.waves ? 160 * 1024 / shape.lds : 16 / shape.waves;
     const int64_t blocks = static_cast<int64_t>(v.nkb) * v.nnb;
     int64_t s = (static_cast<int64_t>(kComputeUnits) * per_cu + blocks - 1) / blocks;
     s = s < v.npanel ? s : v.npanel;
@@ -907,16 +991,16 @@ size_t linear_vjp_workspace_bytes(int64_t M, int K, int N, bool bf16)
 template <typename T, int KC, int NC, bool FromD>
 static hipError_t launch_panel(const PanelArgs &p, int blocks, hipStream_t stream)
 {
-    using S = PanelShape<T, KC, NC>;
-    if (S::lds > 64 * 1024) {
+    constexpr PanelShape S = kPanelShape<T, KC, NC>;
+    if (S.lds > 64 * 1024) {
         static const hipError_t e =
             hipFuncSetAttribute(reinterpret_cast<const void *>(&panel_kernel<T, KC, NC, FromD>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, S::lds);
+                                hipFuncAttributeMaxDynamicSharedMemorySize, S.lds);
         if (e != hipSuccess)
             return e;
     }
     hipLaunchKernelGGL((panel_kernel<T, KC, NC, FromD>), dim3(static_cast<unsigned>(p.nsplit * blocks)),
-                       dim3(64 * S::W), S::lds, stream, p);
+                       dim3(64 * S.waves), S.lds, stream, p);
     return hipGetLastError();
 }
 
