@@ -236,6 +236,52 @@ __device__ __forceinline__ void store_n(T *p, int valid, const float (&v)[8])
     }
 }
 
+// Sixteen bytes of stored values (four floats, eight bf16) as loaded.
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+template <typename T>
+struct RawVec;
+template <>
+struct RawVec<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float *p, int valid) { load_n<4>(p, valid, v); }
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+};
+template <>
+struct RawVec<bf16bits> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const bf16bits *p, int valid) { v = load8(p, valid); }
+    __device__ __forceinline__ float get(int i) const
+    {
+        return __uint_as_float(i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+    }
+};
+
+// N floats (four or eight) as P truncated parts at consecutive places of P
+// planes `plane` elements apart.
+template <int P, int N>
+__device__ __forceinline__ void put_parts(bf16bits *at, int plane, const float (&v)[N])
+{
+    float w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        w[i] = v[i];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        uint32_t u[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            u[i] = high_halves(w[2 * i + 1], w[2 * i]);
+            w[2 * i] = below_high(w[2 * i]);
+            w[2 * i + 1] = below_high(w[2 * i + 1]);
+        }
+        if constexpr (N == 8)
+            *reinterpret_cast<u32x4 *>(at + p * plane) = u32x4{u[0], u[1], u[2], u[3]};
+        else
+            *reinterpret_cast<uint2 *>(at + p * plane) = uint2{u[0], u[1]};
+    }
+}
+
 // acc[k] += the products of parts i of a[k] and j of b up to order i + j =
 // most parts - 1 (three parts: six products; two: three; one against P: P),
 // the smallest first, over all k before the next, so that instructions that

@@ -14,28 +14,6 @@
 
 namespace etp {
 
-template <typename T>
-constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-
-// A vector of kVec values as loaded, turned into floats where they are used.
-template <typename T>
-struct RawVec;
-template <>
-struct RawVec<float> {
-    float v[8];
-    __device__ __forceinline__ void load(const float *p, int valid) { load_n<4>(p, valid, v); }
-    __device__ __forceinline__ float get(int i) const { return v[i]; }
-};
-template <>
-struct RawVec<bf16bits> {
-    u32x4 v;
-    __device__ __forceinline__ void load(const bf16bits *p, int valid) { v = load8(p, valid); }
-    __device__ __forceinline__ float get(int i) const
-    {
-        return __uint_as_float(i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
-    }
-};
-
 template <int Ctrl>
 __device__ __forceinline__ float dpp_add(float v)
 {

@@ -595,16 +595,18 @@ struct PanelArgs {
     int nkb;          // blocks of 32 KC along K (1 with gx)
 };
 
-// Two panels' parts lie in LDS: while one feeds the products the next is
-// formed and written (one barrier a panel). A panel has 64 rows, or 32 where
-// two of 64 would take more than 80 KiB (160 KiB with eight waves, of which a
-// compute unit holds one workgroup either way).
+// With eight waves (one workgroup a compute unit) two panels' parts lie in LDS,
+// and while one feeds the products the next is formed and written: one barrier
+// a panel, of 64 rows, or 32 where two of 64 do not fit. With four waves one
+// panel of 64 rows, so that several workgroups share a compute unit and fill
+// each other's waits.
 struct PanelShape {
-    int px, waves, sx, sd, rows, lds;  // parts of x, row strides (elements)
+    int px, waves, sx, sd, bufs, rows, lds, per_cu;  // parts of x, row strides (elements), workgroups that fit
     constexpr PanelShape(bool bf16, int kc, int nc)
         : px(bf16 ? 1 : 3), waves(kc == 4 || nc == 4 ? 8 : 4), sx(32 * kc + 16), sd(32 * nc + 16),
-          rows(2 * 2 * 64 * (px * sx + 3 * sd) <= (waves == 8 ? 160 : 80) * 1024 ? 64 : 32),
-          lds(2 * 2 * rows * (px * sx + 3 * sd))
+          bufs(waves == 8 ? 2 : 1), rows(2 * bufs * 64 * (px * sx + 3 * sd) <= 160 * 1024 ? 64 : 32),
+          lds(2 * bufs * rows * (px * sx + 3 * sd)),
+          per_cu(waves == 8 ? 1 : 160 * 1024 / lds < 3 ? 160 * 1024 / lds : 3)
     {
     }
 };
@@ -612,13 +614,14 @@ template <typename T, int KC, int NC>
 constexpr PanelShape kPanelShape{sizeof(T) == 2, KC, NC};
 
 template <typename T, int KC, int NC, bool FromD>
-__global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves)) panel_kernel(const PanelArgs p)
+__global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
+                                  (kPanelShape<T, KC, NC>.waves / 4 * kPanelShape<T, KC, NC>.per_cu)) panel_kernel(const PanelArgs p)
 {
     constexpr PanelShape S = kPanelShape<T, KC, NC>;
     constexpr int PX = S.px, W = S.waves, SX = S.sx, SD = S.sd, kRows = S.rows;
     constexpr int kBuf = kRows * (PX * SX + 3 * SD);  // elements of one panel
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    bf16bits *const lds = reinterpret_cast<bf16bits *>(smem);  // [2] of d [3][kRows][SD], x [PX][kRows][SX]
+    bf16bits *const lds = reinterpret_cast<bf16bits *>(smem);  // [bufs] of d [3][kRows][SD], x [PX][kRows][SX]
     const LinearVjpArgs &a = p.v;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
@@ -627,35 +630,36 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves)) panel_ker
     const int K = a.K, N = a.N;
     const bool want_gx = a.gx != nullptr, want_gw = a.gW != nullptr, want_gb = a.gb != nullptr && k0 == 0;
 
-    // loads: wave w takes 16 rows of the panel and every WS-th chunk of 32
-    // columns
-    constexpr int kTiles = kRows / 16, WS = W / kTiles, NL = (NC + WS - 1) / WS, KL = (KC + WS - 1) / WS;
-    const int lrow = 16 * (wave % kTiles) + c, ch0 = wave / kTiles;
-    Raw8<std::conditional_t<FromD, float, T>> gn[NL];
-    Raw8<T> zn[NL], xn[KL];
+    // loads: a thread takes 16 bytes of the same columns in every ND-th (NX-th)
+    // row of the panel, so that a wave covers whole rows (half the width a row
+    // and wave costs a quarter of the bandwidth)
+    using Src = std::conditional_t<FromD, float, T>;
+    constexpr int kTiles = kRows / 16, VD = kVec<Src>, VX = kVec<T>;
+    constexpr int PD = 32 * NC / VD, PK = 32 * KC / VX;   // pieces of a row
+    constexpr int RD = 64 * W / PD, RX = 64 * W / PK;      // rows at a time
+    constexpr int ND = (kRows + RD - 1) / RD, NX = (kRows + RX - 1) / RX;
+    const int drow = threadIdx.x / PD, dcol = threadIdx.x % PD * VD;
+    const int xrow = threadIdx.x / PK, xcol = threadIdx.x % PK * VX;
+    RawVec<Src> gn[ND];
+    RawVec<T> zn[ND], xn[NX];
     auto fetch = [&](int64_t panel) {
-        const int64_t r = panel * kRows + lrow, rc = r < a.M ? r : a.M - 1;
 #pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const int j = j0 + 32 * (ch0 + WS * n) + 8 * q;
-            if (NC % WS && ch0 + WS * n >= NC)
-                continue;
-            const int valid = N - j;
+        for (int n = 0; n < ND; ++n) {
+            const int64_t r = panel * kRows + drow + RD * n, rc = r < a.M ? r : a.M - 1;
+            const int valid = N - j0 - dcol;
             if constexpr (FromD) {
-                gn[n].load(p.d + rc * N + j, valid);
+                gn[n].load(p.d + rc * N + j0 + dcol, valid);
             } else {
-                gn[n].load(static_cast<const T *>(a.gy) + rc * a.ldgy + j, valid);
+                gn[n].load(static_cast<const T *>(a.gy) + rc * a.ldgy + j0 + dcol, valid);
                 if (a.act != kActNone)
-                    zn[n].load(static_cast<const T *>(a.z) + rc * a.ldz + j, valid);
+                    zn[n].load(static_cast<const T *>(a.z) + rc * a.ldz + j0 + dcol, valid);
             }
         }
         if (want_gw) {
 #pragma unroll
-            for (int n = 0; n < KL; ++n) {
-                const int k = k0 + 32 * (ch0 + WS * n) + 8 * q;
-                if (KC % WS && ch0 + WS * n >= KC)
-                    continue;
-                xn[n].load(static_cast<const T *>(a.x) + rc * a.ldx + k, K - k);
+            for (int n = 0; n < NX; ++n) {
+                const int64_t r = panel * kRows + xrow + RX * n, rc = r < a.M ? r : a.M - 1;
+                xn[n].load(static_cast<const T *>(a.x) + rc * a.ldx + k0 + xcol, K - k0 - xcol);
             }
         }
     };
@@ -690,70 +694,70 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves)) panel_ker
 #pragma unroll
         for (int j = 0; j < JT; ++j)
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float gb[NL][8];
+    float gb[VD];
 #pragma unroll
-    for (int n = 0; n < NL; ++n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            gb[n][i] = 0.f;
+    for (int i = 0; i < VD; ++i)
+        gb[i] = 0.f;
 
     // the fetched panel's parts into LDS
     auto put = [&](int64_t panel, bf16bits *dl) __attribute__((always_inline)) {
         bf16bits *xl = dl + 3 * kRows * SD;
-        const bool live = panel * kRows + lrow < a.M;
 #pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const int ch = ch0 + WS * n;
-            if (NC % WS && ch >= NC)
+        for (int n = 0; n < ND; ++n) {
+            const int row = drow + RD * n;
+            if (kRows % RD && row >= kRows)
                 continue;
-            float d[8];
-            gn[n].get(d);
-            if constexpr (!FromD) {
-                if (a.act != kActNone) {
-                    float z[8];
-                    zn[n].get(z);
+            const bool live = panel * kRows + row < a.M;
+            float d[VD];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        d[i] *= act_slope(a.act, z[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < VD; ++i) {
+                d[i] = gn[n].get(i);
+                if (!FromD && a.act != kActNone)
+                    d[i] *= act_slope(a.act, zn[n].get(i));
                 d[i] = live ? d[i] : 0.f;
-                gb[n][i] += d[i];
+                gb[i] += d[i];
             }
-            const Frag<3> f = split8<3>(d);
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-                *reinterpret_cast<bf16x8 *>(dl + (t * kRows + lrow) * SD + 32 * ch + 8 * q) = f.p[t];
+            put_parts<3>(dl + row * SD + dcol, kRows * SD, d);
         }
         if (want_gw) {
 #pragma unroll
-            for (int n = 0; n < KL; ++n) {
-                const int ch = ch0 + WS * n;
-                if (KC % WS && ch >= KC)
+            for (int n = 0; n < NX; ++n) {
+                const int row = xrow + RX * n;
+                if (kRows % RX && row >= kRows)
                     continue;
-                const Frag<PX> f = xn[n].template frag<PX>();
+                if constexpr (PX == 1) {
+                    *reinterpret_cast<u32x4 *>(xl + row * SX + xcol) = xn[n].v;
+                } else {
+                    float x[VX];
 #pragma unroll
-                for (int t = 0; t < PX; ++t)
-                    *reinterpret_cast<bf16x8 *>(xl + (t * kRows + lrow) * SX + 32 * ch + 8 * q) = f.p[t];
+                    for (int i = 0; i < VX; ++i)
+                        x[i] = xn[n].get(i);
+                    put_parts<PX>(xl + row * SX + xcol, kRows * SX, x);
+                }
             }
         }
     };
 
     if (s < p.npanel) {
         fetch(s);
-        put(s, lds);
-        if (s + p.nsplit < p.npanel)
-            fetch(s + p.nsplit);
+        if (S.bufs == 2) {
+            put(s, lds);
+            if (s + p.nsplit < p.npanel)
+                fetch(s + p.nsplit);
+        }
     }
     int buf = 0;
-    for (int64_t panel = s; panel < p.npanel; panel += p.nsplit, buf ^= 1) {
-        // one barrier a panel: the panel's parts are seen by every wave, and
-        // the buffer written next was last read before it
+    for (int64_t panel = s; panel < p.npanel; panel += p.nsplit, buf ^= S.bufs - 1) {
+        if (S.bufs == 1) {
+            put(panel, lds);
+            if (panel + p.nsplit < p.npanel)
+                fetch(panel + p.nsplit);
+        }
+        // the panel's parts are seen by every wave; of two buffers the one
+        // written next was last read before this barrier
         __syncthreads();
         const bf16bits *dl = lds + buf * kBuf, *xl = dl + 3 * kRows * SD;
-        if (panel + p.nsplit < p.npanel) {
+        if (S.bufs == 2 && panel + p.nsplit < p.npanel) {
             put(panel + p.nsplit, lds + (buf ^ 1) * kBuf);
             if (panel + 2 * p.nsplit < p.npanel)
                 fetch(panel + 2 * p.nsplit);
@@ -819,8 +823,11 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves)) panel_ker
                 }
             }
         }
+        if (S.bufs == 1)
+            __syncthreads();  // the next panel overwrites the rows
     }
-    __syncthreads();  // the sums below reuse the space
+    if (S.bufs == 2)
+        __syncthreads();  // the sums below reuse the space
 
     float *part = static_cast<float *>(a.ws) + static_cast<int64_t>(s) * (static_cast<int64_t>(K) + 1) * N;
     if (want_gw) {
@@ -838,29 +845,17 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves)) panel_ker
             }
     }
     if (want_gb) {
-        // over the 16 rows of the lanes, then the row tiles through LDS
-        float *sums = reinterpret_cast<float *>(smem);  // [kTiles][32 NC]
+        // the threads that share columns, through LDS, in row order
+        float *sums = reinterpret_cast<float *>(smem);  // [RD][32 NC]
+        static_assert(RD * 32 * NC * sizeof(float) <= static_cast<size_t>(S.lds));
 #pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const int ch = ch0 + WS * n;
-            if (NC % WS && ch >= NC)
-                continue;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float v = gb[n][i];
-#pragma unroll
-                for (int m = 1; m < 16; m <<= 1)
-                    v += __shfl_xor(v, m);
-                if (c == 0)
-                    sums[(wave % kTiles) * 32 * NC + 32 * ch + 8 * q + i] = v;
-            }
-        }
+        for (int i = 0; i < VD; ++i)
+            sums[drow * 32 * NC + dcol + i] = gb[i];
         __syncthreads();
         for (int j = threadIdx.x; j < 32 * NC; j += 64 * W) {
             float v = 0.f;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-                v += sums[t * 32 * NC + j];
+            for (int r = 0; r < RD; ++r)
+                v += sums[r * 32 * NC + j];
             if (j0 + j < N)
                 part[static_cast<int64_t>(K) * N + j0 + j] = v;
         }
@@ -970,9 +965,8 @@ static VjpCut vjp_cut(int64_t M, int K, int N, bool bf16)
     v.fused = K <= 128 && N <= 128;
     const PanelShape shape(bf16, v.fused ? v.kc : 4, v.fused ? v.nc : 4);
     v.npanel = (M + shape.rows - 1) / shape.rows;
-    const int per_cu = 160 * 1024 / shape.lds < 16 / shape.waves ? 160 * 1024 / shape.lds : 16 / shape.waves;
     const int64_t blocks = static_cast<int64_t>(v.nkb) * v.nnb;
-    int64_t s = (static_cast<int64_t>(kComputeUnits) * per_cu + blocks - 1) / blocks;
+    int64_t s = (static_cast<int64_t>(kComputeUnits) * shape.per_cu + blocks - 1) / blocks;
     s = s < v.npanel ? s : v.npanel;
     v.nsplit = static_cast<int>(s < 1 ? 1 : s);
     v.d_bytes = v.fused ? 0 : (sizeof(float) * static_cast<size_t>(M) * N + 15) / 16 * 16;
