@@ -282,34 +282,26 @@ __device__ __forceinline__ void put_parts(bf16bits *at, int plane, const float (
     }
 }
 
-// acc[k] += the products of parts i of a[k] and j of b up to order i + j =
-// most parts - 1 (three parts: six products; two: three; one against P: P),
-// the smallest first, over all k before the next, so that instructions that
-// follow each other do not wait for each other's result.
-template <int PA, int PB, int N>
-__device__ __forceinline__ void mma(const Frag<PA> (&a)[N], const Frag<PB> &b, f32x4 (&acc)[N])
+// acc[i0 + i][j] += a[i] b[j] for all i and j: the products of part u of a and
+// v of b up to order u + v = most parts - 1 (three parts: six products; two:
+// three; one against P: P), the smallest first, each over all i and j before
+// the next, so that instructions that follow each other do not wait for each
+// other's result.
+template <int PA, int PB, int NA, int NB, int N>
+__device__ __forceinline__ void mma(const Frag<PA> (&a)[NA], const Frag<PB> (&b)[NB], f32x4 (&acc)[N][NB], int i0 = 0)
 {
 #pragma unroll
     for (int s = (PA > PB ? PA : PB) - 1; s >= 0; --s)
 #pragma unroll
-        for (int i = 0; i < PA; ++i)
-            if (s - i >= 0 && s - i < PB) {
+        for (int u = 0; u < PA; ++u)
+            if (s - u >= 0 && s - u < PB) {
 #pragma unroll
-                for (int k = 0; k < N; ++k)
-                    acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[k].p[i], b.p[s - i], acc[k], 0, 0, 0);
+                for (int i = 0; i < NA; ++i)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        acc[i0 + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i].p[u], b[j].p[s - u],
+                                                                                 acc[i0 + i][j], 0, 0, 0);
             }
-}
-
-template <int PA, int PB>
-__device__ __forceinline__ f32x4 mma(const Frag<PA> &a, const Frag<PB> &b, f32x4 acc)
-{
-#pragma unroll
-    for (int s = (PA > PB ? PA : PB) - 1; s >= 0; --s)
-#pragma unroll
-        for (int i = 0; i < PA; ++i)
-            if (s - i >= 0 && s - i < PB)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], acc, 0, 0, 0);
-    return acc;
 }
 
 // Fragment of a contraction that runs along the rows of a row-major bf16

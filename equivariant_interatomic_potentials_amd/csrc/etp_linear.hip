@@ -265,7 +265,7 @@ __device__ __forceinline__ void load_addend(const ProductArgs &a, int64_t row, i
 // The four tiles acc of a 64-column group from column j0 (tile 0's first) of
 // row `row`: epilogue and stores.
 template <typename T, Dense D>
-__device__ __forceinline__ void store_group(const ProductArgs &a, int64_t row, int j0, int q, f32x4 (&acc)[4],
+__device__ __forceinline__ void store_group(const ProductArgs &a, int64_t row, int j0, int q, const f32x4 (&acc)[4][1],
                                             const float (&add)[sizeof(T) == 4 ? 4 : 2][8])
 {
     if (row >= a.M)
@@ -273,14 +273,15 @@ __device__ __forceinline__ void store_group(const ProductArgs &a, int64_t row, i
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            float v[8] = {acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
+            const f32x4 u = acc[t][0];
+            float v[8] = {u[0], u[1], u[2], u[3]};
             store_cols<T, D, 4>(a, row, j0 + col_of_quarter<T>(t, q), v, add[t]);
         }
     } else {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            float v[8] = {acc[2 * t][0],     acc[2 * t][1],     acc[2 * t][2],     acc[2 * t][3],
-                          acc[2 * t + 1][0], acc[2 * t + 1][1], acc[2 * t + 1][2], acc[2 * t + 1][3]};
+            const f32x4 u = acc[2 * t][0], w = acc[2 * t + 1][0];
+            float v[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
             store_cols<T, D, 8>(a, row, j0 + col_of_quarter<T>(2 * t, q), v, add[t]);
         }
     }
@@ -339,25 +340,29 @@ __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs
     if (tile < ntile)
         fetch(tile);
     for (; tile < ntile; tile += nstream * waves) {
-        Frag<kRowParts<T, D>> xf[KC];
+        Frag<kRowParts<T, D>> xf[KC][1];
 #pragma unroll
         for (int kc = 0; kc < KC; ++kc)
-            xf[kc] = next[kc].frag(a);
+            xf[kc][0] = next[kc].frag(a);
         if (tile + nstream * waves < ntile)
             fetch(tile + nstream * waves);
         const int64_t row = tile * 16 + c;
         for (int g = 0; g < nb / 64 && n0 + 64 * g < a.ND; ++g) {
             float add[sizeof(T) == 4 ? 4 : 2][8];
             load_group_addend<T, D>(a, row, n0 + 64 * g, q, add);
-            f32x4 acc[4];
+            f32x4 acc[4][1];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                acc[t] = *reinterpret_cast<const f32x4 *>(bias + 64 * g + col_of_quarter<T>(t, q));
+                acc[t][0] = *reinterpret_cast<const f32x4 *>(bias + 64 * g + col_of_quarter<T>(t, q));
 #pragma unroll
-            for (int kc = 0; kc < KC; ++kc)
+            for (int kc = 0; kc < KC; ++kc) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    acc[t] = mma(Mx::tile(matrix + kc * Mx::chunk(nb), 4 * g + t, nb, lane), xf[kc], acc[t]);
+                for (int t = 0; t < 4; t += 2) {
+                    const bf16bits *m = matrix + kc * Mx::chunk(nb);
+                    const Frag<kParts<T>> w[2] = {Mx::tile(m, 4 * g + t, nb, lane), Mx::tile(m, 4 * g + t + 1, nb, lane)};
+                    mma(w, xf[kc], acc, t);
+                }
+            }
             store_group<T, D>(a, row, n0 + 64 * g, q, acc, add);
         }
     }
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
         return;  // the whole workgroup
     const int n0 = (b8 % ncol) * kCols;
 
-    f32x4 acc[RT][NT];
+    f32x4 acc[NT][RT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int j = n0 + col_of_quarter<T>(t, q);
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-            acc[r][t] = b;
+            acc[t][r] = b;
     }
     const int nk = (a.KD + 32 * SUB - 1) / (32 * SUB);
     RowChunk<T, D> xn[RT][SUB];
@@ -424,12 +429,12 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
 #pragma unroll
             for (int n = 0; n < kItems; ++n)
                 Mx::store(matrix[buf][u], threadIdx.x + 256 * n, kCols, wn[u][n]);
-        Frag<kRowParts<T, D>> xf[RT][SUB];
+        Frag<kRowParts<T, D>> xf[SUB][RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
-                xf[r][u] = xn[r][u].frag(a);
+                xf[u][r] = xn[r][u].frag(a);
         // one barrier a chunk: the stores above are seen by every wave, and
         // the buffer written next was last read before it
         __syncthreads();
@@ -438,11 +443,10 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const auto w = Mx::tile(matrix[buf][u], t, kCols, lane);
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    acc[r][t] = mma(w, xf[r][u], acc[r][t]);
+            for (int t = 0; t < NT; t += 2) {
+                const Frag<kParts<T>> w[2] = {Mx::tile(matrix[buf][u], t, kCols, lane),
+                                              Mx::tile(matrix[buf][u], t + 1, kCols, lane)};
+                mma(w, xf[u], acc, t);
             }
     }
 #pragma unroll
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
             const int64_t row = row0 + 16 * r + c;
             float add[sizeof(T) == 4 ? 4 : 2][8];
             load_group_addend<T, D>(a, row, n0 + 64 * g, q, add);
-            f32x4 v[4] = {acc[r][4 * g], acc[r][4 * g + 1], acc[r][4 * g + 2], acc[r][4 * g + 3]};
+            const f32x4 v[4][1] = {{acc[4 * g][r]}, {acc[4 * g + 1][r]}, {acc[4 * g + 2][r]}, {acc[4 * g + 3][r]}};
             store_group<T, D>(a, row, n0 + 64 * g, q, v, add);
         }
 }
@@ -471,10 +475,10 @@ __global__ void __launch_bounds__(256) product_thin_kernel(const ProductArgs a, 
     const int c = lane & 15, q = lane >> 4;
     const int n0 = (blockIdx.x % ncol) * 64;
     const int64_t row = static_cast<int64_t>(blockIdx.x / ncol) * 16 + c, rc = row < a.M ? row : a.M - 1;
-    f32x4 acc[4];
+    f32x4 acc[4][1];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
-        acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        acc[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int k = 32 * wave; k < a.KD; k += 128) {
         RowChunk<T, D> x;
         x.load(a, rc, k + 8 * q);
@@ -483,15 +487,14 @@ __global__ void __launch_bounds__(256) product_thin_kernel(const ProductArgs a, 
         for (int t = 0; t < 4; ++t)  // this lane's column of tile t: the one whose entry is c
             w[t].load(a, k + 8 * q, n0 + (sizeof(T) == 4 ? 16 * t + c
                                                          : 32 * (t >> 1) + 8 * (c >> 2) + 4 * (t & 1) + (c & 3)));
-        const auto xf = x.frag(a);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            acc[t] = mma(w[t].frag(), xf, acc[t]);
+        const Frag<kRowParts<T, D>> xf[1] = {x.frag(a)};
+        const Frag<kParts<T>> wf[4] = {w[0].frag(), w[1].frag(), w[2].frag(), w[3].frag()};
+        mma(wf, xf, acc);
     }
     if (wave > 0) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            part[wave - 1][t][lane] = acc[t];
+            part[wave - 1][t][lane] = acc[t][0];
     }
     __syncthreads();
     if (wave > 0)
@@ -500,12 +503,12 @@ __global__ void __launch_bounds__(256) product_thin_kernel(const ProductArgs a, 
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
         for (int w = 0; w < 3; ++w)
-            acc[t] += part[w][t][lane];
+            acc[t][0] += part[w][t][lane];
         const int j = n0 + col_of_quarter<T>(t, q);
         if (D == Dense::Fwd && a.bias) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                acc[t][i] += j + i < a.ND ? a.bias[j + i] : 0.f;
+                acc[t][0][i] += j + i < a.ND ? a.bias[j + i] : 0.f;
         }
     }
     float add[sizeof(T) == 4 ? 4 : 2][8];
@@ -635,11 +638,11 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
     // and wave costs a quarter of the bandwidth)
     using Src = std::conditional_t<FromD, float, T>;
     constexpr int kTiles = kRows / 16, VD = kVec<Src>, VX = kVec<T>;
-    constexpr int PD = 32 * NC / VD, PK = 32 * KC / VX;   // pieces of a row
-    constexpr int RD = 64 * W / PD, RX = 64 * W / PK;      // rows at a time
+    constexpr int DP = 32 * NC / VD, XP = 32 * KC / VX;   // pieces of a row
+    constexpr int RD = 64 * W / DP, RX = 64 * W / XP;      // rows at a time
     constexpr int ND = (kRows + RD - 1) / RD, NX = (kRows + RX - 1) / RX;
-    const int drow = threadIdx.x / PD, dcol = threadIdx.x % PD * VD;
-    const int xrow = threadIdx.x / PK, xcol = threadIdx.x % PK * VX;
+    const int drow = threadIdx.x / DP, dcol = threadIdx.x % DP * VD;
+    const int xrow = threadIdx.x / XP, xcol = threadIdx.x % XP * VX;
     RawVec<Src> gn[ND];
     RawVec<T> zn[ND], xn[NX];
     auto fetch = [&](int64_t panel) {
@@ -670,7 +673,7 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
     constexpr int RT = kTiles / RS;
     const int grp = wave % groups, rt0 = (wave / groups) * RT;
     const bool gx_wave = want_gx && wave / groups < RS;
-    Frag<PX> wf[G][NC];
+    Frag<PX> wf[NC][G];
     if (gx_wave) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -681,7 +684,7 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
                 Raw8<T> raw;
                 raw.load(static_cast<const T *>(a.W) + static_cast<int64_t>(k < K ? k : 0) * N + j,
                          k < K ? N - j : 0);
-                wf[g][n] = raw.template frag<PX>();
+                wf[n][g] = raw.template frag<PX>();
             }
     }
 
@@ -763,24 +766,26 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
                 fetch(panel + 2 * p.nsplit);
         }
         if (gx_wave) {
-            constexpr int PD = sizeof(T) == 4 ? 3 : 2;
+            constexpr int PD = sizeof(T) == 4 ? 3 : 2;  // parts of d that a bf16 gx needs
+            f32x4 o[G][RT];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                f32x4 o[G];
+            for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int g = 0; g < G; ++g)
-                    o[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int r = 0; r < RT; ++r)
+                    o[g][r] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    Frag<PD> df;
+            for (int n = 0; n < NC; ++n) {
+                Frag<PD> df[RT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
 #pragma unroll
                     for (int t = 0; t < PD; ++t)
-                        df.p[t] = *reinterpret_cast<const bf16x8 *>(
+                        df[r].p[t] = *reinterpret_cast<const bf16x8 *>(
                             dl + (t * kRows + 16 * (rt0 + r) + c) * SD + 32 * n + 8 * q);
+                mma(wf[n], df, o);
+            }
 #pragma unroll
-                    for (int g = 0; g < G; ++g)
-                        o[g] = mma(wf[g][n], df, o[g]);
-                }
+            for (int r = 0; r < RT; ++r) {
                 const int64_t row = panel * kRows + 16 * (rt0 + r) + c;
                 const int k = sizeof(T) == 4 ? 16 * grp + 4 * q : 32 * grp + 8 * q;
                 if (row < a.M && k < K) {
@@ -790,7 +795,7 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
                     for (int g = 0; g < G; ++g)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            v[4 * g + i] = o[g][i];
+                            v[4 * g + i] = o[g][r][i];
                     if (a.accumulate) {
                         float was[8];
                         load_n<4 * G>(dst, K - k, was);
@@ -811,15 +816,16 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
 #pragma unroll
                     for (int t = 0; t < 3; ++t)
                         df[j].p[t] = read_transposed(dl + t * kRows * SD, SD, st, 16 * (jt0 + j), lane);
+                constexpr int KS = KT < 2 ? KT : 2;  // row tiles at a time
 #pragma unroll
-                for (int i = 0; i < KT; ++i) {
-                    Frag<PX> xf;
+                for (int i = 0; i < KT; i += KS) {
+                    Frag<PX> xf[KS];
 #pragma unroll
-                    for (int t = 0; t < PX; ++t)
-                        xf.p[t] = read_transposed(xl + t * kRows * SX, SX, st, 16 * (kt0 + i), lane);
+                    for (int k = 0; k < KS; ++k)
 #pragma unroll
-                    for (int j = 0; j < JT; ++j)
-                        acc[i][j] = mma(xf, df[j], acc[i][j]);
+                        for (int t = 0; t < PX; ++t)
+                            xf[k].p[t] = read_transposed(xl + t * kRows * SX, SX, st, 16 * (kt0 + i + k), lane);
+                    mma(xf, df, acc, i);
                 }
             }
         }

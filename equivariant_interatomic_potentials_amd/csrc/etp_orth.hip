@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
             x[i] = *reinterpret_cast<const f32x4 *>(xs + i * 256);
     }
 
-    f32x4 acc[OMAX];
+    f32x4 acc[OMAX][1];
     // acc = this strip's part of A = X X^T
     auto gram = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -177,34 +177,34 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < OMAX; ++k)
-            acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+            acc[k][0] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ch = 0; ch < W / 2; ++ch) {
-            Frag<P> fj, fi[OMAX];
+            Frag<P> fj[1], fi[OMAX];
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                fj.p[p] = read_transposed(pl + p * kPlane, SN, ch, 16 * tj, lane);
+                fj[0].p[p] = read_transposed(pl + p * kPlane, SN, ch, 16 * tj, lane);
 #pragma unroll
             for (int k = 0; k < OMAX; ++k)
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    fi[k].p[p] = NH == 1 && k == 0 ? fj.p[p]
+                    fi[k].p[p] = NH == 1 && k == 0 ? fj[0].p[p]
                                                    : read_transposed(pl + p * kPlane, SN, ch, 16 * row_tile(k), lane);
             mma(fi, fj, acc);
         }
         __syncthreads();
     };
     // the tiles of a symmetric matrix (and their mirror images) into LDS
-    auto put_tiles = [&](const f32x4 (&t)[OMAX]) __attribute__((always_inline)) {
+    auto put_tiles = [&](const f32x4 (&t)[OMAX][1]) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < OMAX; ++k)
             if (has(k)) {
                 const int i = row_tile(k);
-                put4<P>(pl + (16 * tj + c) * SN + slot_of(16 * i + 4 * q), kPlane, t[k]);
+                put4<P>(pl + (16 * tj + c) * SN + slot_of(16 * i + 4 * q), kPlane, t[k][0]);
                 if (i != tj) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        float v = t[k][r];
+                        float v = t[k][0][r];
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
                             const bf16bits u = from_f32<bf16bits>(v);
@@ -219,22 +219,22 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
     // X <- a X + (b A + c A^2) X, with A's tiles in acc
     auto update = [&]() __attribute__((always_inline)) {
         put_tiles(acc);
-        f32x4 sq[OMAX];
+        f32x4 sq[OMAX][1];
 #pragma unroll
         for (int k = 0; k < OMAX; ++k)
-            sq[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+            sq[k][0] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ch = 0; ch < NT / 2; ++ch) {
-            Frag<P> fj, fi[OMAX];
+            Frag<P> fj[1], fi[OMAX];
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                fj.p[p] = *reinterpret_cast<const bf16x8 *>(pl + p * kPlane + (16 * tj + c) * SN + 32 * ch + 8 * q);
+                fj[0].p[p] = *reinterpret_cast<const bf16x8 *>(pl + p * kPlane + (16 * tj + c) * SN + 32 * ch + 8 * q);
 #pragma unroll
             for (int k = 0; k < OMAX; ++k)
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     fi[k].p[p] = NH == 1 && k == 0
-                                     ? fj.p[p]
+                                     ? fj[0].p[p]
                                      : *reinterpret_cast<const bf16x8 *>(
                                            pl + p * kPlane + (16 * row_tile(k) + c) * SN + 32 * ch + 8 * q);
             mma(fi, fj, sq);
@@ -242,24 +242,24 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < OMAX; ++k)
-            acc[k] = cb * acc[k] + cc * sq[k];
+            acc[k][0] = cb * acc[k][0] + cc * sq[k][0];
         put_tiles(acc);
-        Frag<P> fx[NT / 2];
+        Frag<P> fx[NT / 2][1];
 #pragma unroll
         for (int ch = 0; ch < NT / 2; ++ch) {
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] = x[2 * ch + (i >> 2)][i & 3];
-            fx[ch] = split8_rounded<P>(v);
+            fx[ch][0] = split8_rounded<P>(v);
         }
         constexpr int R = NT < 4 ? NT : 4;  // row tiles at a time
 #pragma unroll
         for (int i = 0; i < NT; i += R) {
-            f32x4 y[R];
+            f32x4 y[R][1];
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                y[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+                y[r][0] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ch = 0; ch < NT / 2; ++ch) {
                 Frag<P> fp[R];
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
             }
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                x[i + r] = ca * x[i + r] + y[r];  // one rounding at the size of X, not one per product
+                x[i + r] = ca * x[i + r] + y[r][0];  // one rounding at the size of X, not one per product
         }
         __syncthreads();
     };
@@ -296,18 +296,18 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
                 float *out = s.a_out + static_cast<int64_t>(blockIdx.x) * set + own;
 #pragma unroll
                 for (int i = 0; i < OMAX; ++i)
-                    *reinterpret_cast<f32x4 *>(out + i * 256) = acc[i];
+                    *reinterpret_cast<f32x4 *>(out + i * 256) = acc[i][0];
                 return;
             }
         } else {
 #pragma unroll
             for (int i = 0; i < OMAX; ++i)
-                acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
             for (int p = 0; p < s.strips; ++p) {
                 const float *in = s.a_in + (static_cast<int64_t>(b) * s.strips + p) * set + own;
 #pragma unroll
                 for (int i = 0; i < OMAX; ++i)
-                    acc[i] += *reinterpret_cast<const f32x4 *>(in + i * 256);
+                    acc[i][0] += *reinterpret_cast<const f32x4 *>(in + i * 256);
             }
         }
         update();
@@ -415,13 +415,7 @@ __global__ void __launch_bounds__(512) orth_product_kernel(const OrthProductArgs
                 fa[i].p[p] = *reinterpret_cast<const bf16x8 *>(la + buf * kBuf + (p * kOT + wr + 16 * i + c) * SK + 8 * q);
                 fb[i].p[p] = *reinterpret_cast<const bf16x8 *>(lb + buf * kBuf + (p * kOT + wc + 16 * i + c) * SK + 8 * q);
             }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            f32x4 t[2] = {acc[0][j], acc[1][j]};
-            mma(fa, fb[j], t);
-            acc[0][j] = t[0];
-            acc[1][j] = t[1];
-        }
+        mma(fa, fb, acc);
     }
     __syncthreads();
     float *mine = tile + grp * kOT * SO;
