@@ -61,7 +61,17 @@ __device__ __forceinline__ Frag<P> split8(const float (&v)[8])
     return f;
 }
 
-// The same with rounded instead of truncated parts (nearest even): the dropped
+// A workgroup barrier for what goes through LDS: it waits for this wave's LDS
+// accesses, and not, as __syncthreads does, for its loads from memory, so that
+// what was asked for ahead stays in flight across it.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// split8 with rounded instead of truncated parts (nearest even): the dropped
 // products are smaller and of either sign, at the same cost, but values above
 // the largest bf16 (3.39e38) would become infinite.
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

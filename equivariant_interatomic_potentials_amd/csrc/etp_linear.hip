@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs
     }
     for (int i = threadIdx.x; i < nb; i += blockDim.x)
         bias[i] = a.bias && n0 + i < a.ND ? a.bias[n0 + i] : 0.f;
-    __syncthreads();
+    lds_barrier();
 
     RowChunk<T, D> next[KC];
     auto fetch = [&](int64_t tile) {
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
                 xf[u][r] = xn[r][u].frag(a);
         // one barrier a chunk: the stores above are seen by every wave, and
         // the buffer written next was last read before it
-        __syncthreads();
+        lds_barrier();
         if (it + 1 < nk)
             fetch(it + 1);
 #pragma unroll
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(256) product_thin_kernel(const ProductArgs a, 
         for (int t = 0; t < 4; ++t)
             part[wave - 1][t][lane] = acc[t][0];
     }
-    __syncthreads();
+    lds_barrier();
     if (wave > 0)
         return;
 #pragma unroll
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
         }
         // the panel's parts are seen by every wave; of two buffers the one
         // written next was last read before this barrier
-        __syncthreads();
+        lds_barrier();
         const bf16bits *dl = lds + buf * kBuf, *xl = dl + 3 * kRows * SD;
         if (S.bufs == 2 && panel + p.nsplit < p.npanel) {
             put(panel + p.nsplit, lds + (buf ^ 1) * kBuf);
@@ -830,10 +830,10 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
             }
         }
         if (S.bufs == 1)
-            __syncthreads();  // the next panel overwrites the rows
+            lds_barrier();  // the next panel overwrites the rows
     }
     if (S.bufs == 2)
-        __syncthreads();  // the sums below reuse the space
+        lds_barrier();  // the sums below reuse the space
 
     float *part = static_cast<float *>(a.ws) + static_cast<int64_t>(s) * (static_cast<int64_t>(K) + 1) * N;
     if (want_gw) {
@@ -857,7 +857,7 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
 #pragma unroll
         for (int i = 0; i < VD; ++i)
             sums[drow * 32 * NC + dcol + i] = gb[i];
-        __syncthreads();
+        lds_barrier();
         for (int j = threadIdx.x; j < 32 * NC; j += 64 * W) {
             float v = 0.f;
             for (int r = 0; r < RD; ++r)
@@ -914,7 +914,7 @@ __global__ void __launch_bounds__(Cols * Ways) sum_parts_kernel(const int64_t n0
     }
     lds[ty][tx] = v;
     for (int d = Ways / 2; d; d >>= 1) {
-        __syncthreads();
+        lds_barrier();
         if (ty < d)
             lds[ty][tx] += lds[ty + d][tx];
     }

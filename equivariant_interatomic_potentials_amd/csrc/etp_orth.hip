@@ -2,11 +2,14 @@
 // X <- a X + (b A + c A^2) X, A = X X^T, on X / (|X|_F + eps). Everywhere X is
 // n x m with n <= m (a tall matrix is read and written transposed).
 //
-// All products run on the matrix cores on bf16 parts (etp_dense_mma.hpp): three
-// for float matrices, whose small singular values the steps amplify by up to
-// a^5, so that every product has to be of float quality; two (2^-16) for bf16
-// ones, whose result is rounded to 2^-8. A and P = b A + c A^2 are symmetric:
-// the tiles on and above the diagonal are formed and mirrored.
+// All products run on the matrix cores on rounded bf16 parts
+// (etp_dense_mma.hpp): three for float matrices, whose small singular values
+// the steps amplify by up to a^5, so that every product has to be of float
+// quality; two (2^-17, three instructions) for bf16 ones, whose result is
+// rounded to 2^-9. (One half float of 11 bits would do for large matrices of
+// many directions, but loses 0.4% on a single one, where its roundings do not
+// average out.) A and P = b A + c A^2 are symmetric: only tiles on one side of
+// the diagonal are formed.
 //
 //  * n <= 128: orth_strip_kernel, a workgroup per 16 W <= 128 columns. The
 //    strip of X stays in registers for all steps (a wave holds 16 columns, all
@@ -30,22 +33,32 @@ constexpr int kOrthParts = sizeof(T) == 4 ? 3 : 2;
 
 constexpr int kNormParts = 64;  // partial sums of squares per matrix
 
-// part[b][p] = sum of squares of slice p of matrix b, in double
+// part[b][p] = sum of squares of slice p of matrix b (whole 16-byte vectors,
+// the odd end in the last slice), in double
 template <typename T>
 __global__ void __launch_bounds__(256) orth_norm_kernel(const T *__restrict__ G, const int64_t count,
                                                         double *__restrict__ part)
 {
     __shared__ double lds[256];
+    constexpr int V = kVec<T>;
     const T *g = G + blockIdx.y * count;
-    const int64_t i0 = count * blockIdx.x / kNormParts, i1 = count * (blockIdx.x + 1) / kNormParts;
+    const int64_t nv = count / V;
+    const int64_t i0 = nv * blockIdx.x / kNormParts, i1 = nv * (blockIdx.x + 1) / kNormParts;
     double s = 0.0;
     for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
-        const double v = to_f32(g[i]);
+        RawVec<T> v;
+        v.load(g + i * V, V);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            s = __builtin_fma(static_cast<double>(v.get(k)), static_cast<double>(v.get(k)), s);
+    }
+    if (blockIdx.x == kNormParts - 1 && threadIdx.x < count % V) {
+        const double v = to_f32(g[nv * V + threadIdx.x]);
         s = __builtin_fma(v, v, s);
     }
     lds[threadIdx.x] = s;
     for (int d = 128; d; d >>= 1) {
-        __syncthreads();
+        lds_barrier();
         if (threadIdx.x < d)
             lds[threadIdx.x] += lds[threadIdx.x + d];
     }
@@ -70,8 +83,9 @@ struct StripArgs {
     int n, m, tall;
     int strips;          // workgroups per matrix
     int step;            // -1: first launch of several (scale, partial A); else the step; all steps if strips = 1
-    const double *norm;  // partial sums of squares (strips > 1)
-    float *xs;           // X between launches, in register order
+    const double *norm;  // partial sums of squares, or null: summed by the strip kernel
+    const float *x_in;   // X between launches, in register order
+    float *x_out;
     const float *a_in;   // partial A of this launch's X, in register order
     float *a_out;
 };
@@ -90,17 +104,30 @@ __device__ __forceinline__ void put4(bf16bits *at, int plane, f32x4 v)
     }
 }
 
-// Place of column j of A and P within an LDS row: in each 32 columns, the four
-// from 4 q and the four from 16 + 4 q lie together, as the eight contraction
-// slots that a lane of quarter q holds (of X in registers, and so of A).
-__device__ __forceinline__ int slot_of(int j) { return (j & ~31) + 8 * ((j >> 2) & 3) + 4 * ((j >> 4) & 1) + (j & 3); }
+// One tile (four of the eight slots) of a fragment of rows 16 r .. + 15 of a
+// symmetric matrix, contraction over its column tile k: read as it lies, or,
+// where only the mirror tile is stored, read transposed from there.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ s16x4 symmetric_half(const bf16bits *m, int stride, int r, int k, bool stored, int lane)
+{
+    typedef __attribute__((address_space(3))) s16x4 *lds4;
+    const int c = lane & 15, q = lane >> 4;
+    if (stored)
+        return *reinterpret_cast<const s16x4 *>(m + (16 * r + c) * stride + 16 * k + 4 * q);
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds4)(m + (16 * k + 4 * q + (c >> 2)) * stride + 16 * r + 4 * (c & 3)));
+}
 
-// NT tiles of 16 rows, W waves of 16 columns; NT <= W.
-template <typename T, int NT, int W>
+// NT tiles of 16 rows, W waves; H waves share 16 columns (one launch per step
+// only: each holds the columns' old X and forms NT / H of their row tiles).
+template <typename T, int NT, int W, int H>
 __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 {
-    constexpr int P = kOrthParts<T>, SN = 16 * NT + 16;  // LDS row stride (elements)
-    constexpr int kPlane = 16 * W * SN;                  // X^T: 16 W rows; A, P: 16 NT rows
+    // LDS row stride (elements): rows start 4 or more banks apart, so neither
+    // 16 rows of 8 bytes nor 4 rows of 32 collide
+    constexpr int P = kOrthParts<T>, SN = 16 * NT + 24;
+    constexpr int S = W / H, NR = NT / H;                 // column groups, row tiles a wave forms
+    constexpr int kPlane = 16 * (S > NT ? S : NT) * SN;   // X^T: 16 S rows; A, P: 16 NT rows
     constexpr int NH = W / NT, OMAX = (NT / 2 + NH) / NH;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     bf16bits *pl = reinterpret_cast<bf16bits *>(smem);  // [P][kPlane]
@@ -108,23 +135,23 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
     const int b = blockIdx.x / s.strips, g = blockIdx.x % s.strips;
-    const int n = s.n, m = s.m, col = 16 * W * g + 16 * wave + c;
+    const int n = s.n, m = s.m, grp = wave % S, col = 16 * S * g + 16 * grp + c;
     const int64_t nm = static_cast<int64_t>(n) * m;
     const float ca = s.o.coef[0], cb = s.o.coef[1], cc = s.o.coef[2];
 
-    // this wave's tiles of A: column tile j, row tiles j + o for every NH-th
-    // offset o up to half way round (each pair of tiles once)
-    const int tj = wave % NT, th = wave / NT;
-    auto row_tile = [&](int k) { return (tj + th + NH * k) % NT; };
-    // (an offset past that is computed like the others, and not used)
-    auto has = [&](int k) {
-        const int o = th + NH * k;
-        return o <= NT / 2 && !(2 * o == NT && 2 * tj >= NT);
-    };
+    // this wave's tiles of A: column tile tj, row tiles tj + o for every NH-th
+    // offset o up to half way round (mod NT): each pair of tiles once, those
+    // half way round twice. Tile (tj + o, tj) is stored as row tile tj, column
+    // tile tj + o: rows r hold the columns up to half way round after r.
+    int tj = wave % NT;
+    const int th = wave / NT;
+    auto mine = [&](int o) { return NH == 1 || o % NH == th; };
+    auto around = [&](int o) { return (tj + o) % NT; };
 
     // the strip: x[i][r] = X[16 i + 4 q + r][col]
     f32x4 x[NT];
-    float *xs = s.xs + (static_cast<int64_t>(blockIdx.x) * W + wave) * NT * 256 + lane * 4;
+    const float *xs = s.x_in + (static_cast<int64_t>(blockIdx.x) * S + grp) * NT * 256 + lane * 4;
+    float *xs_out = s.x_out + (static_cast<int64_t>(blockIdx.x) * S + grp) * NT * 256 + lane * 4;
     if (s.strips == 1 || s.step < 0) {
         const T *G = static_cast<const T *>(s.o.G) + b * nm;
 #pragma unroll
@@ -138,26 +165,26 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
                               : 0.f;
             }
         float scale;
-        if (s.strips == 1) {
+        if (s.norm) {
+            scale = orth_scale(s.norm, b, s.o.eps);
+        } else {
+            // all of the matrix by every workgroup of it
             double t = 0.0;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    t = __builtin_fma(static_cast<double>(x[i][r]), static_cast<double>(x[i][r]), t);
+            for (int64_t i = threadIdx.x; i < nm; i += 64 * W) {
+                const double v = to_f32(G[i]);
+                t = __builtin_fma(v, v, t);
+            }
 #pragma unroll
             for (int d = 32; d; d >>= 1)
                 t += __shfl_xor(t, d);
             if (lane == 0)
                 red[wave] = t;
-            __syncthreads();
+            lds_barrier();
             t = red[0];
 #pragma unroll
             for (int w = 1; w < W; ++w)
                 t += red[w];
             scale = static_cast<float>(1.0 / (sqrt(t) + s.o.eps));
-        } else {
-            scale = orth_scale(s.norm, b, s.o.eps);
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -168,18 +195,22 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
             x[i] = *reinterpret_cast<const f32x4 *>(xs + i * 256);
     }
 
-    f32x4 acc[OMAX][1];
+    f32x4 acc[OMAX][1];  // offset o at o / NH
     // acc = this strip's part of A = X X^T
     auto gram = [&]() __attribute__((always_inline)) {
+        // the tiles' LDS addresses are worked out anew in every step: kept over
+        // the steps they would take a register each, and spill
+        asm volatile("" : "+s"(tj));
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-            put4<P>(pl + (16 * wave + c) * SN + 16 * i + 4 * q, kPlane, x[i]);
-        __syncthreads();
+            if (H == 1 || i / NR == wave / S)
+                put4<P>(pl + (16 * grp + c) * SN + 16 * i + 4 * q, kPlane, x[i]);
+        lds_barrier();
 #pragma unroll
         for (int k = 0; k < OMAX; ++k)
             acc[k][0] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ch = 0; ch < W / 2; ++ch) {
+        for (int ch = 0; ch < S / 2; ++ch) {
             Frag<P> fj[1], fi[OMAX];
 #pragma unroll
             for (int p = 0; p < P; ++p)
@@ -188,62 +219,70 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
             for (int k = 0; k < OMAX; ++k)
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    fi[k].p[p] = NH == 1 && k == 0 ? fj[0].p[p]
-                                                   : read_transposed(pl + p * kPlane, SN, ch, 16 * row_tile(k), lane);
+                    fi[k].p[p] = NH == 1 && k == 0
+                                     ? fj[0].p[p]
+                                     : read_transposed(pl + p * kPlane, SN, ch, 16 * around(NH * k + th), lane);
             mma(fi, fj, acc);
+            __builtin_amdgcn_sched_barrier(0);  // one chunk's fragments at a time are what the registers hold
         }
-        __syncthreads();
+        lds_barrier();
     };
-    // the tiles of a symmetric matrix (and their mirror images) into LDS
-    auto put_tiles = [&](const f32x4 (&t)[OMAX][1]) __attribute__((always_inline)) {
+    auto put_tiles = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < OMAX; ++k)
-            if (has(k)) {
-                const int i = row_tile(k);
-                put4<P>(pl + (16 * tj + c) * SN + slot_of(16 * i + 4 * q), kPlane, t[k][0]);
-                if (i != tj) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float v = t[k][0][r];
-#pragma unroll
-                        for (int p = 0; p < P; ++p) {
-                            const bf16bits u = from_f32<bf16bits>(v);
-                            pl[p * kPlane + (16 * i + 4 * q + r) * SN + slot_of(16 * tj + c)] = u;
-                            v -= to_f32(u);
-                        }
-                    }
-                }
-            }
-        __syncthreads();
+        for (int o = 0; o <= NT / 2; ++o)
+            if (mine(o))
+                put4<P>(pl + (16 * tj + c) * SN + 16 * around(o) + 4 * q, kPlane, acc[o / NH][0]);
+        lds_barrier();
     };
     // X <- a X + (b A + c A^2) X, with A's tiles in acc
     auto update = [&]() __attribute__((always_inline)) {
-        put_tiles(acc);
+        asm volatile("" : "+s"(tj));
+        put_tiles();
         f32x4 sq[OMAX][1];
 #pragma unroll
         for (int k = 0; k < OMAX; ++k)
             sq[k][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // the contraction goes round from tj, so that what is stored and what
+        // is mirrored is known here
+        auto half = [&](int o, int k, int p) __attribute__((always_inline)) {  // row tile tj + o, column tile tj + k
+            return symmetric_half(pl + p * kPlane, SN, around(o), around(k), (k - o + NT) % NT <= NT / 2, lane);
+        };
 #pragma unroll
-        for (int ch = 0; ch < NT / 2; ++ch) {
-            Frag<P> fj[1], fi[OMAX];
+        for (int k = 0; k < NT; k += 2) {
+            Frag<P> fj[1];
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                fj[0].p[p] = *reinterpret_cast<const bf16x8 *>(pl + p * kPlane + (16 * tj + c) * SN + 32 * ch + 8 * q);
+                fj[0].p[p] = __builtin_bit_cast(
+                    bf16x8, __builtin_shufflevector(half(0, k, p), half(0, k + 1, p), 0, 1, 2, 3, 4, 5, 6, 7));
+            if constexpr (NH == 1) {
+                Frag<P> fi[OMAX];
+                fi[0] = fj[0];
 #pragma unroll
-            for (int k = 0; k < OMAX; ++k)
+                for (int o = 1; o <= NT / 2; ++o)
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    fi[k].p[p] = NH == 1 && k == 0
-                                     ? fj[0].p[p]
-                                     : *reinterpret_cast<const bf16x8 *>(
-                                           pl + p * kPlane + (16 * row_tile(k) + c) * SN + 32 * ch + 8 * q);
-            mma(fi, fj, sq);
+                    for (int p = 0; p < P; ++p)
+                        fi[o].p[p] = __builtin_bit_cast(
+                            bf16x8, __builtin_shufflevector(half(o, k, p), half(o, k + 1, p), 0, 1, 2, 3, 4, 5, 6, 7));
+                mma(fi, fj, sq);
+                __builtin_amdgcn_sched_barrier(0);
+            } else {
+#pragma unroll
+                for (int o = 0; o <= NT / 2; ++o)
+                    if (mine(o)) {
+                        Frag<P> fi[1];
+#pragma unroll
+                        for (int p = 0; p < P; ++p)
+                            fi[0].p[p] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(half(o, k, p), half(o, k + 1, p),
+                                                                                            0, 1, 2, 3, 4, 5, 6, 7));
+                        mma(fi, fj, sq, o / NH);
+                    }
+            }
         }
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int k = 0; k < OMAX; ++k)
             acc[k][0] = cb * acc[k][0] + cc * sq[k][0];
-        put_tiles(acc);
+        put_tiles();
         Frag<P> fx[NT / 2][1];
 #pragma unroll
         for (int ch = 0; ch < NT / 2; ++ch) {
@@ -253,9 +292,11 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
                 v[i] = x[2 * ch + (i >> 2)][i & 3];
             fx[ch][0] = split8_rounded<P>(v);
         }
-        constexpr int R = NT < 4 ? NT : 4;  // row tiles at a time
+        constexpr int R = NR < 4 ? NR : 4;  // row tiles at a time
 #pragma unroll
         for (int i = 0; i < NT; i += R) {
+            if (H > 1 && i / NR != wave / S)
+                continue;
             f32x4 y[R][1];
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -266,16 +307,21 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        fp[r].p[p] = *reinterpret_cast<const bf16x8 *>(pl + p * kPlane + (16 * (i + r) + c) * SN +
-                                                                       32 * ch + 8 * q);
+                    for (int p = 0; p < P; ++p) {
+                        s16x4 h[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            h[u] = symmetric_half(pl + p * kPlane, SN, i + r, 2 * ch + u,
+                                                  (2 * ch + u - i - r + NT) % NT <= NT / 2, lane);
+                        fp[r].p[p] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                    }
                 mma(fp, fx[ch], y);
             }
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 x[i + r] = ca * x[i + r] + y[r][0];  // one rounding at the size of X, not one per product
         }
-        __syncthreads();
+        lds_barrier();
     };
 
     // one strip: all steps; else the launch's part of one: (the strips' sum of
@@ -289,7 +335,8 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
             if (!one) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
-                    *reinterpret_cast<f32x4 *>(xs + i * 256) = x[i];
+                    if (H == 1 || i / NR == wave / S)
+                        *reinterpret_cast<f32x4 *>(xs_out + i * 256) = x[i];
             }
             gram();
             if (!one) {
@@ -303,11 +350,22 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 #pragma unroll
             for (int i = 0; i < OMAX; ++i)
                 acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-            for (int p = 0; p < s.strips; ++p) {
-                const float *in = s.a_in + (static_cast<int64_t>(b) * s.strips + p) * set + own;
+            for (int p = 0; p < s.strips; p += 4) {  // four sets in flight, added in order
+                f32x4 in[4][OMAX];
 #pragma unroll
-                for (int i = 0; i < OMAX; ++i)
-                    acc[i][0] += *reinterpret_cast<const f32x4 *>(in + i * 256);
+                for (int u = 0; u < 4; ++u) {
+                    const int64_t at = static_cast<int64_t>(b) * s.strips + (p + u < s.strips ? p + u : p);
+#pragma unroll
+                    for (int i = 0; i < OMAX; ++i)
+                        in[u][i] = *reinterpret_cast<const f32x4 *>(s.a_in + at * set + own + i * 256);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (p + u < s.strips) {
+#pragma unroll
+                        for (int i = 0; i < OMAX; ++i)
+                            acc[i][0] += in[u][i];
+                    }
             }
         }
         update();
@@ -321,7 +379,7 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = 16 * i + 4 * q + r;
-            if (row < n && col < m)
+            if ((H == 1 || i / NR == wave / S) && row < n && col < m)
                 X[s.tall ? static_cast<int64_t>(col) * n + row : static_cast<int64_t>(row) * m + col] =
                     from_f32<T>(x[i][r]);
         }
@@ -330,13 +388,21 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 // ---------------------------------------------------------- large matrices
 
 // A matrix [rows][cols] as bf16 parts in global memory, rows and columns
-// padded with zeros to multiples of 64: part p of element (r, c) of matrix b
-// at ((b P + p) rows + r) cols + c.
+// padded with zeros to multiples of 64, each part of a matrix in fragment
+// order: 16 rows by 32 columns together, as the 64 lanes hold them, so that a
+// wave's fragment is 1 KiB without a gap (16 rows of 64 bytes each take about
+// three times as long to load). Place of entry (row, col) of a part, col a
+// multiple of eight:
+__device__ __forceinline__ int64_t part_place(int row, int col, int cols)
+{
+    return (static_cast<int64_t>(row >> 4) * (cols >> 5) + (col >> 5)) * 512 + (((col >> 3) & 3) * 16 + (row & 15)) * 8;
+}
 
 enum class OrthOp { Gram, Poly, Apply };
 
 struct OrthProductArgs {
     int rows, cols, depth;     // padded sizes of the result and the contraction
+    int tiles, mats;           // per matrix, matrices
     const bf16bits *A, *B;     // [rows][depth], [cols][depth]
     const bf16bits *D;         // added with weight beta: A itself (Poly), X (Apply)
     float alpha, beta;
@@ -348,139 +414,155 @@ struct OrthProductArgs {
 constexpr int kOT = 64;  // tile
 
 // Results are alpha A B^T + beta D in 64 x 64 tiles. Both operands lie along
-// the contraction (X^T is kept beside X, and A, P are symmetric). Two groups
-// of four waves (32 x 32 each) take alternate chunks of 32 of the contraction
-// through their own double-buffered LDS tiles, a 16-byte load per thread and
-// part, and are added at the end: a few hundred tiles are all there are, so
-// the compute unit's second set of waves has to come from the same tile. The
-// tile leaves through LDS, so that it can be written along its rows and along
-// its columns.
+// the contraction (X^T is kept beside X, and A, P are symmetric). There are a
+// few hundred tiles at most, so a tile takes a whole compute unit: its four
+// waves each form all of it over every fourth chunk of 64 (32 with three parts) of the contraction,
+// with fragments straight from memory into registers (nothing is shared
+// before the end, so nothing goes through LDS and no wave waits for another;
+// one wave to a SIMD has the registers for the next chunk's 24 or 16 KiB while
+// it works on this one), and the four are added in wave order. The tile leaves
+// through LDS, so that it can be written along its rows and along its columns.
+constexpr int kOrthOut = kOT + 4;  // LDS row stride of the tile (floats)
+
 template <typename T, OrthOp Op>
-__global__ void __launch_bounds__(512) orth_product_kernel(const OrthProductArgs a)
+__global__ void __launch_bounds__(256, 1) orth_product_kernel(const OrthProductArgs a)
 {
-    constexpr int P = kOrthParts<T>, SK = 40, SO = kOT + 4;
-    constexpr int kBuf = P * kOT * SK;  // elements of one operand's chunk
-    static_assert(8 * kBuf * sizeof(bf16bits) >= 2 * kOT * SO * sizeof(float));
+    constexpr int P = kOrthParts<T>, SO = kOrthOut, NH = P == 2 ? 2 : 1, KC = 32 * NH;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
-    bf16bits *la = reinterpret_cast<bf16bits *>(smem) + grp * 4 * kBuf, *lb = la + 2 * kBuf;  // [2][P][64][SK] each
-    float *tile = reinterpret_cast<float *>(smem);                                            // [2][64][SO]
+    float *tile = reinterpret_cast<float *>(smem);  // [4][64][SO]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = lane & 15, q = lane >> 4, b = blockIdx.y;
+    const int c = lane & 15, q = lane >> 4;
+    // workgroups b and b + 8 run on the same XCD: each XCD takes a run of
+    // consecutive tiles, so that it fetches few rows of the operands (every
+    // launch begins with cold caches, and an XCD gets 0.6 TB/s from beyond
+    // its own)
+    const int w = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    if (w >= a.tiles * a.mats)
+        return;  // the whole workgroup: padding to a multiple of 8
+    const int b = w / a.tiles, t = w - b * a.tiles;
     int ti, tj;
     if constexpr (Op == OrthOp::Apply) {
-        ti = blockIdx.x % (a.rows / kOT);
-        tj = blockIdx.x / (a.rows / kOT);
+        ti = t % (a.rows / kOT);
+        tj = t / (a.rows / kOT);
     } else {  // tiles on and above the diagonal: tj (tj + 1) / 2 + ti
         tj = 0;
-        ti = blockIdx.x;
+        ti = t;
         while (ti > tj)
             ti -= ++tj;
     }
     const int r0 = ti * kOT, c0 = tj * kOT;
-    const bf16bits *A = a.A + static_cast<int64_t>(b) * P * a.rows * a.depth;
-    const bf16bits *B = a.B + static_cast<int64_t>(b) * P * a.cols * a.depth;
-    const int lr = (threadIdx.x >> 2) & 63, lk = (threadIdx.x & 3) * 8;
+    const int64_t pa = static_cast<int64_t>(a.rows) * a.depth, pb = static_cast<int64_t>(a.cols) * a.depth;  // a part
+    const int64_t band = static_cast<int64_t>(a.depth) * 16;                                              // 16 rows
+    const bf16bits *A = a.A + b * P * pa + (r0 >> 4) * band + lane * 8;
+    const bf16bits *B = a.B + b * P * pb + (c0 >> 4) * band + lane * 8;
 
-    u32x4 na[P], nb[P];
-    auto fetch = [&](int k) {
+    Frag<P> fa[2][NH][4], fb[2][NH][4];  // [buffer][half][tile]
+    auto fetch = [&](int ch, int buf) __attribute__((always_inline)) {
+        if (KC * ch >= a.depth)
+            return;
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            na[p] = *reinterpret_cast<const u32x4 *>(A + (static_cast<int64_t>(p) * a.rows + r0 + lr) * a.depth + k + lk);
-            nb[p] = *reinterpret_cast<const u32x4 *>(B + (static_cast<int64_t>(p) * a.cols + c0 + lr) * a.depth + k + lk);
-        }
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    fa[buf][h][i].p[p] =
+                        *reinterpret_cast<const bf16x8 *>(A + p * pa + i * band + (NH * ch + h) * 512);
+                    fb[buf][h][i].p[p] =
+                        *reinterpret_cast<const bf16x8 *>(B + p * pb + i * band + (NH * ch + h) * 512);
+                }
     };
-    f32x4 acc[2][2];
+    f32x4 acc[4][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 4; ++j)
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int wr = ((wave >> 1) & 1) * 32, wc = (wave & 1) * 32;
-    fetch(32 * grp);
-    for (int k = 32 * grp, buf = 0; k < a.depth; k += 64, buf ^= 1) {  // depth is a multiple of 64
+    fetch(wave, 0);
+    for (int ch = wave; KC * ch < a.depth; ch += 8) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            *reinterpret_cast<u32x4 *>(la + buf * kBuf + (p * kOT + lr) * SK + lk) = na[p];
-            *reinterpret_cast<u32x4 *>(lb + buf * kBuf + (p * kOT + lr) * SK + lk) = nb[p];
+        for (int u = 0; u < 2; ++u) {
+            if (KC * (ch + 4 * u) >= a.depth)
+                break;
+            fetch(ch + 4 * u + 4, u ^ 1);
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+                mma(fa[u][h], fb[u][h], acc);
         }
-        __syncthreads();
-        if (k + 64 < a.depth)
-            fetch(k + 64);
-        Frag<P> fa[2], fb[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                fa[i].p[p] = *reinterpret_cast<const bf16x8 *>(la + buf * kBuf + (p * kOT + wr + 16 * i + c) * SK + 8 * q);
-                fb[i].p[p] = *reinterpret_cast<const bf16x8 *>(lb + buf * kBuf + (p * kOT + wc + 16 * i + c) * SK + 8 * q);
-            }
-        mma(fa, fb, acc);
     }
-    __syncthreads();
-    float *mine = tile + grp * kOT * SO;
+    float *mine = tile + wave * kOT * SO;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                mine[(wr + 16 * i + 4 * q + r) * SO + wc + 16 * j + c] = acc[i][j][r];
-    __syncthreads();
-    // thread: row orow, eight columns from oc of the tile
+                mine[(16 * i + 4 * q + r) * SO + 16 * j + c] = acc[i][j][r];
+    lds_barrier();
+    // thread: rows orow + 32 h, eight columns from oc of the tile
     const int orow = threadIdx.x >> 3, oc = (threadIdx.x & 7) * 8;
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = a.alpha * (tile[orow * SO + oc + i] + tile[kOT * SO + orow * SO + oc + i]);
-    if (Op != OrthOp::Gram) {
-#pragma unroll
-        for (int p = P - 1; p >= 0; --p) {
-            const bf16bits *d = a.D + ((static_cast<int64_t>(b) * P + p) * a.rows + r0 + orow) * a.cols + c0 + oc;
-            float f[8];
-            load8(d, 8, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = __builtin_fmaf(a.beta, f[i], v[i]);
-        }
-    }
     const bool last = Op == OrthOp::Apply && a.last;
-    if (last && !a.tall) {
-        if (r0 + orow < a.n)
-            store8(static_cast<T *>(a.last) + (static_cast<int64_t>(b) * a.n + r0 + orow) * a.m + c0 + oc,
-                   a.m - c0 - oc, v);
-        return;
-    }
     // out [rows][cols], and out_t [cols][rows] (for a symmetric result the
     // same matrix)
-    auto put = [&](bf16bits *o, int row, int col, int R, int C) {
+    auto put = [&](bf16bits *o, int row, int col, int R, int C, const float (&v)[8]) {
         const Frag<P> f = split8_rounded<P>(v);
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            *reinterpret_cast<bf16x8 *>(o + ((static_cast<int64_t>(b) * P + p) * R + row) * C + col) = f.p[p];
+            *reinterpret_cast<bf16x8 *>(o + (static_cast<int64_t>(b) * P + p) * R * C + part_place(row, col, C)) = f.p[p];
     };
-    if (!last)
-        put(a.out, r0 + orow, c0 + oc, a.rows, a.cols);
-    if (Op != OrthOp::Apply && ti == tj)
+    float v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = orow + 32 * h;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float *t = tile + row * SO + oc + i;
+            v[h][i] = a.alpha * ((t[0] + t[kOT * SO]) + (t[2 * kOT * SO] + t[3 * kOT * SO]));
+        }
+        if (Op != OrthOp::Gram) {
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p) {
+                float f[8];
+                load8(a.D + (static_cast<int64_t>(b) * P + p) * a.rows * a.cols + part_place(r0 + row, c0 + oc, a.cols), 8, f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[h][i] = __builtin_fmaf(a.beta, f[i], v[h][i]);
+            }
+        }
+        if (!last)
+            put(a.out, r0 + row, c0 + oc, a.rows, a.cols, v[h]);
+        else if (!a.tall && r0 + row < a.n)
+            store8(static_cast<T *>(a.last) + (static_cast<int64_t>(b) * a.n + r0 + row) * a.m + c0 + oc, a.m - c0 - oc,
+                   v[h]);
+    }
+    if (last ? !a.tall : Op != OrthOp::Apply && ti == tj)
         return;
     // back through the tile for the transpose (with what was added)
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        tile[orow * SO + oc + i] = v[i];
-    __syncthreads();
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = tile[(oc + i) * SO + orow];
-    if (!last)
-        put(a.out_t, c0 + orow, r0 + oc, a.cols, a.rows);
-    else if (c0 + orow < a.m)
-        store8(static_cast<T *>(a.last) + (static_cast<int64_t>(b) * a.m + c0 + orow) * a.n + r0 + oc, a.n - r0 - oc, v);
+        for (int i = 0; i < 8; ++i)
+            tile[(orow + 32 * h) * SO + oc + i] = v[h][i];
+    lds_barrier();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = orow + 32 * h;
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = tile[(oc + i) * SO + row];
+        if (!last)
+            put(a.out_t, c0 + row, r0 + oc, a.cols, a.rows, w);
+        else if (c0 + row < a.m)
+            store8(static_cast<T *>(a.last) + (static_cast<int64_t>(b) * a.m + c0 + row) * a.n + r0 + oc, a.n - r0 - oc, w);
+    }
 }
 
-// X = G scale as parts, and X^T: a 64 x 64 tile of X per workgroup
+// X = G scale as parts, and X^T: a 64 x 64 tile of X per workgroup, eight
+// values a thread and store
 template <typename T>
-__global__ void __launch_bounds__(256) orth_split_kernel(const T *__restrict__ G, const double *__restrict__ norm,
+__global__ void __launch_bounds__(512) orth_split_kernel(const T *__restrict__ G, const double *__restrict__ norm,
                                                          const float eps, const int n, const int m, const int tall,
                                                          const int np, const int mp, bf16bits *__restrict__ X,
                                                          bf16bits *__restrict__ XT)
@@ -488,37 +570,44 @@ __global__ void __launch_bounds__(256) orth_split_kernel(const T *__restrict__ G
     constexpr int P = kOrthParts<T>;
     __shared__ float tile[kOT][kOT + 1];  // as G lies: rows of X, or rows of X^T when tall
     const int b = blockIdx.y, rt = np / kOT, r0 = (blockIdx.x % rt) * kOT, c0 = (blockIdx.x / rt) * kOT;
-    const float scale = orth_scale(norm, b, eps);
-    const T *g = G + static_cast<int64_t>(b) * n * m;
+    const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 8;
     const int gr0 = tall ? c0 : r0, gc0 = tall ? r0 : c0, gr = tall ? m : n, gc = tall ? n : m;
-    for (int i = threadIdx.x; i < kOT * kOT; i += 256) {
-        const int r = i >> 6, c = i & 63;
-        tile[r][c] = gr0 + r < gr && gc0 + c < gc ? to_f32(g[static_cast<int64_t>(gr0 + r) * gc + gc0 + c]) * scale
-                                                  : 0.f;
-    }
-    __syncthreads();
-    for (int k = 0; k < 2; ++k) {  // X, then X^T
-        const bool turn = (k == 1) != (tall != 0);
-        bf16bits *o = k ? XT : X;
-        const int R = k ? mp : np, C = k ? np : mp, o0 = k ? c0 : r0, o1 = k ? r0 : c0;
-        for (int i = threadIdx.x; i < kOT * kOT; i += 256) {
-            const int r = i >> 6, c = i & 63;
-            float v = turn ? tile[c][r] : tile[r][c];
+    const int valid = gr0 + row < gr ? gc - gc0 - col : 0;
+    float v[8];
+    load8(G + (static_cast<int64_t>(b) * gr + (valid > 0 ? gr0 + row : 0)) * gc + (valid > 0 ? gc0 + col : 0), valid, v);
+    const float scale = orth_scale(norm, b, eps);
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                o[((static_cast<int64_t>(b) * P + p) * R + o0 + r) * C + o1 + c] =
-                    from_f32<bf16bits>(v);
-                v -= to_f32(from_f32<bf16bits>(v));
-            }
-        }
+    for (int i = 0; i < 8; ++i) {
+        v[i] *= scale;
+        tile[row][col + i] = v[i];
     }
+    auto put = [&](bf16bits *o, int R, int C, int o0, int o1) {
+        const Frag<P> f = split8_rounded<P>(v);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            *reinterpret_cast<bf16x8 *>(o + (static_cast<int64_t>(b) * P + p) * R * C + part_place(o0 + row, o1 + col, C)) =
+                f.p[p];
+    };
+    if (tall)
+        put(XT, mp, np, c0, r0);
+    else
+        put(X, np, mp, r0, c0);
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = tile[col + i][row];
+    if (tall)
+        put(X, np, mp, r0, c0);
+    else
+        put(XT, mp, np, c0, r0);
 }
 
 // ---------------------------------------------------------------- dispatch
 
 struct OrthCut {
     int n, m, tall;
-    int nt, w, strips;        // strip kernel (n <= 128)
+    int nt, w, h, strips;     // strip kernel (n <= 128)
+    bool own_norm;            // the strip kernel sums the squares itself
     int np, mp;               // padded sizes (larger)
     size_t norm, xs, as;      // bytes of the workspace's pieces
     size_t x, a;
@@ -533,19 +622,31 @@ static OrthCut orth_cut(int B, int rows, int cols, bool bf16)
     c.n = c.tall ? cols : rows;
     c.m = c.tall ? rows : cols;
     const size_t b = static_cast<size_t>(B);
-    c.norm = up256(b * kNormParts * sizeof(double));
     if (c.n <= 128) {
         auto tiles = [](int v) { return v <= 32 ? 2 : v <= 64 ? 4 : 8; };
         c.nt = tiles(c.n);
         c.w = tiles(c.m);
-        c.strips = (c.m + 127) / 128;
+        // A workgroup takes 128 columns, or, where more than 64 rows leave
+        // most compute units without a matrix, 64 or 32 of them (H = 2, 4
+        // waves to 16 columns): ORTH_NOTE
+        c.h = 1;
+        if (c.nt == 8)
+            for (int h = 4; h > 1 && c.h == 1; h /= 2)
+                if (static_cast<int64_t>(B) * ((c.m + 128 / h - 1) / (128 / h)) <= 256 && c.m <= 256 * 4 / h)
+                    c.h = h;
+        const int wide = 16 * c.w / c.h;
+        c.strips = (c.m + wide - 1) / wide;
+        c.own_norm = static_cast<int64_t>(c.n) * c.m <= 32768;
+        if (!c.own_norm)
+            c.norm = up256(b * kNormParts * sizeof(double));
         if (c.strips > 1) {
             const int nh = c.w / c.nt, omax = (c.nt / 2 + nh) / nh;
-            c.xs = up256(b * c.strips * c.w * c.nt * 256 * sizeof(float));
+            c.xs = up256(b * c.strips * (c.w / c.h) * c.nt * 256 * sizeof(float));
             c.as = up256(b * c.strips * c.w * omax * 256 * sizeof(float));
         }
         return c;
     }
+    c.norm = up256(b * kNormParts * sizeof(double));
     c.np = (c.n + kOT - 1) / kOT * kOT;
     c.mp = (c.m + kOT - 1) / kOT * kOT;
     const size_t parts = bf16 ? kOrthParts<bf16bits> : kOrthParts<float>;
@@ -557,20 +658,20 @@ static OrthCut orth_cut(int B, int rows, int cols, bool bf16)
 size_t orthogonalize_workspace_bytes(int B, int rows, int cols, bool bf16)
 {
     const OrthCut c = orth_cut(B, rows, cols, bf16);
-    return c.norm + c.xs + 2 * c.as + 4 * c.x + 2 * c.a;
+    return c.norm + 2 * c.xs + 2 * c.as + 4 * c.x + 2 * c.a;
 }
 
-template <typename T, int NT, int W>
+template <typename T, int NT, int W, int H = 1>
 static hipError_t launch_strips(const StripArgs &s, hipStream_t stream)
 {
-    constexpr size_t lds = sizeof(bf16bits) * kOrthParts<T> * 16 * W * (16 * NT + 16);
+    constexpr size_t lds = sizeof(bf16bits) * kOrthParts<T> * 16 * (W / H > NT ? W / H : NT) * (16 * NT + 24);
     if (lds > 64 * 1024) {
-        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_strip_kernel<T, NT, W>),
+        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_strip_kernel<T, NT, W, H>),
                                                         hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL((orth_strip_kernel<T, NT, W>), dim3(static_cast<unsigned>(s.o.B) * s.strips), dim3(64 * W), lds,
+    hipLaunchKernelGGL((orth_strip_kernel<T, NT, W, H>), dim3(static_cast<unsigned>(s.o.B) * s.strips), dim3(64 * W), lds,
                        stream, s);
     return hipGetLastError();
 }
@@ -584,21 +685,26 @@ static hipError_t strips_by_shape(const StripArgs &s, const OrthCut &c, hipStrea
     case 28: return launch_strips<T, 2, 8>(s, stream);
     case 44: return launch_strips<T, 4, 4>(s, stream);
     case 48: return launch_strips<T, 4, 8>(s, stream);
-    default: return launch_strips<T, 8, 8>(s, stream);
+    default:
+        return c.h == 4   ? launch_strips<T, 8, 8, 4>(s, stream)
+               : c.h == 2 ? launch_strips<T, 8, 8, 2>(s, stream)
+                          : launch_strips<T, 8, 8>(s, stream);
     }
 }
 
 template <typename T, OrthOp Op>
-static hipError_t launch_orth_product(const OrthProductArgs &a, dim3 grid, hipStream_t stream)
+static hipError_t launch_orth_product(const OrthProductArgs &a, hipStream_t stream)
 {
-    constexpr size_t lds = 8 * kOrthParts<T> * kOT * 40 * sizeof(bf16bits);
-    if (lds > 64 * 1024) {
-        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_product_kernel<T, Op>),
-                                                        hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess)
-            return e;
-    }
-    hipLaunchKernelGGL((orth_product_kernel<T, Op>), grid, dim3(512), lds, stream, a);
+    constexpr size_t lds = 4 * kOT * kOrthOut * sizeof(float);
+    static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_product_kernel<T, Op>),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess)
+        return e;
+    const int64_t work = static_cast<int64_t>(a.tiles) * a.mats;
+    if (work > 0x7FFFFFF0)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL((orth_product_kernel<T, Op>), dim3(static_cast<unsigned>((work + 7) / 8 * 8)), dim3(256), lds,
+                       stream, a);
     return hipGetLastError();
 }
 
@@ -611,20 +717,26 @@ static hipError_t orthogonalize(const OrthArgs &o, hipStream_t stream)
     ws += c.norm;
     const T *G = static_cast<const T *>(o.G);
     hipError_t e = hipSuccess;
-    if (c.nt && c.strips == 1) {
-        const StripArgs s{o, c.n, c.m, c.tall, 1, 0, nullptr, nullptr, nullptr, nullptr};
-        return strips_by_shape<T>(s, c, stream);
+    if (!c.own_norm) {
+        hipLaunchKernelGGL(orth_norm_kernel<T>, dim3(kNormParts, o.B), dim3(256), 0, stream, G,
+                           static_cast<int64_t>(c.n) * c.m, norm);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
     }
-    hipLaunchKernelGGL(orth_norm_kernel<T>, dim3(kNormParts, o.B), dim3(256), 0, stream, G,
-                       static_cast<int64_t>(c.n) * c.m, norm);
-    if ((e = hipGetLastError()) != hipSuccess)
-        return e;
     if (c.nt) {
-        StripArgs s{o, c.n, c.m, c.tall, c.strips, -1, norm, reinterpret_cast<float *>(ws), nullptr, nullptr};
-        float *as[2] = {reinterpret_cast<float *>(ws + c.xs), reinterpret_cast<float *>(ws + c.xs + c.as)};
-        for (; s.step < o.steps && e == hipSuccess; ++s.step) {  // reads one set of partial sums, writes the other
-            s.a_in = as[s.step & 1];
-            s.a_out = as[(s.step + 1) & 1];
+        StripArgs s{o, c.n, c.m, c.tall, c.strips, c.strips == 1 ? 0 : -1, c.own_norm ? nullptr : norm, nullptr, nullptr,
+                    nullptr, nullptr};
+        if (c.strips == 1)
+            return strips_by_shape<T>(s, c, stream);
+        // each launch reads one set of X and partial sums and writes the other
+        float *xs[2] = {reinterpret_cast<float *>(ws), reinterpret_cast<float *>(ws + c.xs)};
+        float *as[2] = {reinterpret_cast<float *>(ws + 2 * c.xs), reinterpret_cast<float *>(ws + 2 * c.xs + c.as)};
+        for (; s.step < o.steps && e == hipSuccess; ++s.step) {
+            const int i = s.step & 1;
+            s.x_in = xs[i];
+            s.x_out = xs[i ^ 1];
+            s.a_in = as[i];
+            s.a_out = as[i ^ 1];
             e = strips_by_shape<T>(s, c, stream);
         }
         return e;
@@ -633,18 +745,18 @@ static hipError_t orthogonalize(const OrthArgs &o, hipStream_t stream)
     bf16bits *XT[2] = {reinterpret_cast<bf16bits *>(ws + 2 * c.x), reinterpret_cast<bf16bits *>(ws + 3 * c.x)};
     bf16bits *A = reinterpret_cast<bf16bits *>(ws + 4 * c.x), *Q = reinterpret_cast<bf16bits *>(ws + 4 * c.x + c.a);
     const unsigned rt = c.np / kOT, ct = c.mp / kOT;
-    hipLaunchKernelGGL(orth_split_kernel<T>, dim3(rt * ct, o.B), dim3(256), 0, stream, G, norm, o.eps, c.n, c.m,
+    hipLaunchKernelGGL(orth_split_kernel<T>, dim3(rt * ct, o.B), dim3(512), 0, stream, G, norm, o.eps, c.n, c.m,
                        c.tall, c.np, c.mp, X[0], XT[0]);
-    const dim3 sym(rt * (rt + 1) / 2, o.B), all(rt * ct, o.B);
+    const int sym = static_cast<int>(rt * (rt + 1) / 2), all = static_cast<int>(rt * ct);
     for (int k = 0; k < o.steps; ++k) {
         const int i = k & 1;
-        const OrthProductArgs ga{c.np, c.np, c.mp, X[i], X[i], nullptr, 1.f, 0.f, A, A, nullptr, c.n, c.m, c.tall};
-        const OrthProductArgs gp{c.np, c.np, c.np, A, A, A, o.coef[2], o.coef[1], Q, Q, nullptr, c.n, c.m, c.tall};
-        const OrthProductArgs gx{c.np, c.mp, c.np, Q, XT[i], X[i], 1.f, o.coef[0], X[i ^ 1], XT[i ^ 1],
+        const OrthProductArgs ga{c.np, c.np, c.mp, sym, o.B, X[i], X[i], nullptr, 1.f, 0.f, A, A, nullptr, c.n, c.m, c.tall};
+        const OrthProductArgs gp{c.np, c.np, c.np, sym, o.B, A, A, A, o.coef[2], o.coef[1], Q, Q, nullptr, c.n, c.m, c.tall};
+        const OrthProductArgs gx{c.np, c.mp, c.np, all, o.B, Q, XT[i], X[i], 1.f, o.coef[0], X[i ^ 1], XT[i ^ 1],
                                  k + 1 == o.steps ? o.X : nullptr, c.n, c.m, c.tall};
-        if ((e = launch_orth_product<T, OrthOp::Gram>(ga, sym, stream)) != hipSuccess ||
-            (e = launch_orth_product<T, OrthOp::Poly>(gp, sym, stream)) != hipSuccess ||
-            (e = launch_orth_product<T, OrthOp::Apply>(gx, all, stream)) != hipSuccess)
+        if ((e = launch_orth_product<T, OrthOp::Gram>(ga, stream)) != hipSuccess ||
+            (e = launch_orth_product<T, OrthOp::Poly>(gp, stream)) != hipSuccess ||
+            (e = launch_orth_product<T, OrthOp::Apply>(gx, stream)) != hipSuccess)
             return e;
     }
     return hipSuccess;
