@@ -129,7 +129,7 @@ struct MatrixLds {
     static constexpr int P = kParts<T>;
     static constexpr bool kRows = D == Dense::Fwd;
     // elements of one chunk of nb columns
-    static __host__ __device__ constexpr int chunk(int nb) { return kRows ? P * 32 * (nb + 16) : P * 32 * nb; }
+    static __host__ __device__ constexpr int chunk(int nb) { return kRows ? P * 32 * (nb + 8) : P * 32 * nb; }
     // pieces of eight elements of one chunk
     static __host__ __device__ constexpr int pieces(int nb) { return 4 * nb; }
 
@@ -156,7 +156,7 @@ struct MatrixLds {
             const int k = i / (nb / 8), j = i % (nb / 8) * 8, r = 16 * ((k >> 2) & 1) + 4 * (k >> 3) + (k & 3);
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                bf16bits *at = m + (p * 32 + r) * (nb + 16);
+                bf16bits *at = m + (p * 32 + r) * (nb + 8);
                 if constexpr (sizeof(T) == 4) {
                     *reinterpret_cast<bf16x8 *>(at + j) = f.p[p];
                 } else {  // columns 32 g + 8 q .. + 3 and .. + 7: entries 4 q .. + 3 of tiles 2 g and 2 g + 1
@@ -179,7 +179,7 @@ struct MatrixLds {
         Frag<P> f;
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            f.p[p] = kRows ? read_transposed(m + p * 32 * (nb + 16), nb + 16, 0, 16 * t, lane)
+            f.p[p] = kRows ? read_transposed(m + p * 32 * (nb + 8), nb + 8, 0, 16 * t, lane)
                            : *reinterpret_cast<const bf16x8 *>(m + ((t * P + p) * 64 + lane) * 8);
         return f;
     }
@@ -319,6 +319,17 @@ __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs
     if (stream * waves >= ntile)
         return;  // the whole workgroup: padding of the last group of 8
     const int n0 = s * nb;
+    RowChunk<T, D> next[KC];
+    auto fetch = [&](int64_t tile) {
+        const int64_t row = tile * 16 + c, rc = row < a.M ? row : a.M - 1;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc)
+            next[kc].load(a, rc, 32 * kc + 8 * q);
+    };
+    // the first rows are on their way while the matrix is laid out
+    int64_t tile = stream * waves + wave;
+    if (tile < ntile)
+        fetch(tile);
     for (int i = threadIdx.x; i < KC * Mx::pieces(nb); i += blockDim.x) {
         const int kc = i / Mx::pieces(nb), j = i % Mx::pieces(nb);
         Raw8<T> v;
@@ -328,17 +339,6 @@ __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs
     for (int i = threadIdx.x; i < nb; i += blockDim.x)
         bias[i] = a.bias && n0 + i < a.ND ? a.bias[n0 + i] : 0.f;
     lds_barrier();
-
-    RowChunk<T, D> next[KC];
-    auto fetch = [&](int64_t tile) {
-        const int64_t row = tile * 16 + c, rc = row < a.M ? row : a.M - 1;
-#pragma unroll
-        for (int kc = 0; kc < KC; ++kc)
-            next[kc].load(a, rc, 32 * kc + 8 * q);
-    };
-    int64_t tile = stream * waves + wave;
-    if (tile < ntile)
-        fetch(tile);
     for (; tile < ntile; tile += nstream * waves) {
         Frag<kRowParts<T, D>> xf[KC][1];
 #pragma unroll
@@ -606,8 +606,8 @@ struct PanelArgs {
 struct PanelShape {
     int px, waves, sx, sd, bufs, rows, lds, per_cu;  // parts of x, row strides (elements), workgroups that fit
     constexpr PanelShape(bool bf16, int kc, int nc)
-        : px(bf16 ? 1 : 3), waves(kc == 4 || nc == 4 ? 8 : 4), sx(32 * kc + 16), sd(32 * nc + 16),
-          bufs(waves == 8 ? 2 : 1), rows(2 * bufs * 64 * (px * sx + 3 * sd) <= 160 * 1024 ? 64 : 32),
+        : px(bf16 ? 1 : 3), waves(kc == 4 || nc == 4 ? 8 : 4), sx(32 * kc + 8), sd(32 * nc + 8),
+          bufs(waves == 8 ? 2 : 1), rows(2 * bufs * 64 * (px * sx + 3 * sd) <= 144 * 1024 ? 64 : 32),
           lds(2 * bufs * rows * (px * sx + 3 * sd)),
           per_cu(waves == 8 ? 1 : 160 * 1024 / lds < 3 ? 160 * 1024 / lds : 3)
     {

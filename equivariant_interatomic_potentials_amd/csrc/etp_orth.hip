@@ -118,16 +118,14 @@ __device__ __forceinline__ s16x4 symmetric_half(const bf16bits *m, int stride, i
         (lds4)(m + (16 * k + 4 * q + (c >> 2)) * stride + 16 * r + 4 * (c & 3)));
 }
 
-// NT tiles of 16 rows, W waves; H waves share 16 columns (one launch per step
-// only: each holds the columns' old X and forms NT / H of their row tiles).
-template <typename T, int NT, int W, int H>
+// NT tiles of 16 rows, W waves of 16 columns; NT <= W.
+template <typename T, int NT, int W>
 __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 {
     // LDS row stride (elements): rows start 4 or more banks apart, so neither
     // 16 rows of 8 bytes nor 4 rows of 32 collide
     constexpr int P = kOrthParts<T>, SN = 16 * NT + 24;
-    constexpr int S = W / H, NR = NT / H;                 // column groups, row tiles a wave forms
-    constexpr int kPlane = 16 * (S > NT ? S : NT) * SN;   // X^T: 16 S rows; A, P: 16 NT rows
+    constexpr int kPlane = 16 * W * SN;  // X^T: 16 W rows; A, P: 16 NT rows
     constexpr int NH = W / NT, OMAX = (NT / 2 + NH) / NH;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     bf16bits *pl = reinterpret_cast<bf16bits *>(smem);  // [P][kPlane]
@@ -135,7 +133,7 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
     const int b = blockIdx.x / s.strips, g = blockIdx.x % s.strips;
-    const int n = s.n, m = s.m, grp = wave % S, col = 16 * S * g + 16 * grp + c;
+    const int n = s.n, m = s.m, col = 16 * W * g + 16 * wave + c;
     const int64_t nm = static_cast<int64_t>(n) * m;
     const float ca = s.o.coef[0], cb = s.o.coef[1], cc = s.o.coef[2];
 
@@ -150,8 +148,8 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 
     // the strip: x[i][r] = X[16 i + 4 q + r][col]
     f32x4 x[NT];
-    const float *xs = s.x_in + (static_cast<int64_t>(blockIdx.x) * S + grp) * NT * 256 + lane * 4;
-    float *xs_out = s.x_out + (static_cast<int64_t>(blockIdx.x) * S + grp) * NT * 256 + lane * 4;
+    const float *xs = s.x_in + (static_cast<int64_t>(blockIdx.x) * W + wave) * NT * 256 + lane * 4;
+    float *xs_out = s.x_out + (static_cast<int64_t>(blockIdx.x) * W + wave) * NT * 256 + lane * 4;
     if (s.strips == 1 || s.step < 0) {
         const T *G = static_cast<const T *>(s.o.G) + b * nm;
 #pragma unroll
@@ -203,14 +201,13 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
         asm volatile("" : "+s"(tj));
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-            if (H == 1 || i / NR == wave / S)
-                put4<P>(pl + (16 * grp + c) * SN + 16 * i + 4 * q, kPlane, x[i]);
+            put4<P>(pl + (16 * wave + c) * SN + 16 * i + 4 * q, kPlane, x[i]);
         lds_barrier();
 #pragma unroll
         for (int k = 0; k < OMAX; ++k)
             acc[k][0] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ch = 0; ch < S / 2; ++ch) {
+        for (int ch = 0; ch < W / 2; ++ch) {
             Frag<P> fj[1], fi[OMAX];
 #pragma unroll
             for (int p = 0; p < P; ++p)
@@ -292,11 +289,9 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
                 v[i] = x[2 * ch + (i >> 2)][i & 3];
             fx[ch][0] = split8_rounded<P>(v);
         }
-        constexpr int R = NR < 4 ? NR : 4;  // row tiles at a time
+        constexpr int R = NT < 4 ? NT : 4;  // row tiles at a time
 #pragma unroll
         for (int i = 0; i < NT; i += R) {
-            if (H > 1 && i / NR != wave / S)
-                continue;
             f32x4 y[R][1];
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -335,8 +330,7 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
             if (!one) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
-                    if (H == 1 || i / NR == wave / S)
-                        *reinterpret_cast<f32x4 *>(xs_out + i * 256) = x[i];
+                    *reinterpret_cast<f32x4 *>(xs_out + i * 256) = x[i];
             }
             gram();
             if (!one) {
@@ -379,7 +373,7 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = 16 * i + 4 * q + r;
-            if ((H == 1 || i / NR == wave / S) && row < n && col < m)
+            if (row < n && col < m)
                 X[s.tall ? static_cast<int64_t>(col) * n + row : static_cast<int64_t>(row) * m + col] =
                     from_f32<T>(x[i][r]);
         }
@@ -606,7 +600,7 @@ __global__ void __launch_bounds__(512) orth_split_kernel(const T *__restrict__ G
 
 struct OrthCut {
     int n, m, tall;
-    int nt, w, h, strips;     // strip kernel (n <= 128)
+    int nt, w, strips;        // strip kernel (n <= 128)
     bool own_norm;            // the strip kernel sums the squares itself
     int np, mp;               // padded sizes (larger)
     size_t norm, xs, as;      // bytes of the workspace's pieces
@@ -622,31 +616,20 @@ static OrthCut orth_cut(int B, int rows, int cols, bool bf16)
     c.n = c.tall ? cols : rows;
     c.m = c.tall ? rows : cols;
     const size_t b = static_cast<size_t>(B);
+    c.norm = up256(b * kNormParts * sizeof(double));
     if (c.n <= 128) {
         auto tiles = [](int v) { return v <= 32 ? 2 : v <= 64 ? 4 : 8; };
         c.nt = tiles(c.n);
         c.w = tiles(c.m);
-        // A workgroup takes 128 columns, or, where more than 64 rows leave
-        // most compute units without a matrix, 64 or 32 of them (H = 2, 4
-        // waves to 16 columns): ORTH_NOTE
-        c.h = 1;
-        if (c.nt == 8)
-            for (int h = 4; h > 1 && c.h == 1; h /= 2)
-                if (static_cast<int64_t>(B) * ((c.m + 128 / h - 1) / (128 / h)) <= 256 && c.m <= 256 * 4 / h)
-                    c.h = h;
-        const int wide = 16 * c.w / c.h;
-        c.strips = (c.m + wide - 1) / wide;
+        c.strips = (c.m + 127) / 128;
         c.own_norm = static_cast<int64_t>(c.n) * c.m <= 32768;
-        if (!c.own_norm)
-            c.norm = up256(b * kNormParts * sizeof(double));
         if (c.strips > 1) {
             const int nh = c.w / c.nt, omax = (c.nt / 2 + nh) / nh;
-            c.xs = up256(b * c.strips * (c.w / c.h) * c.nt * 256 * sizeof(float));
+            c.xs = up256(b * c.strips * c.w * c.nt * 256 * sizeof(float));
             c.as = up256(b * c.strips * c.w * omax * 256 * sizeof(float));
         }
         return c;
     }
-    c.norm = up256(b * kNormParts * sizeof(double));
     c.np = (c.n + kOT - 1) / kOT * kOT;
     c.mp = (c.m + kOT - 1) / kOT * kOT;
     const size_t parts = bf16 ? kOrthParts<bf16bits> : kOrthParts<float>;
@@ -661,17 +644,17 @@ size_t orthogonalize_workspace_bytes(int B, int rows, int cols, bool bf16)
     return c.norm + 2 * c.xs + 2 * c.as + 4 * c.x + 2 * c.a;
 }
 
-template <typename T, int NT, int W, int H = 1>
+template <typename T, int NT, int W>
 static hipError_t launch_strips(const StripArgs &s, hipStream_t stream)
 {
-    constexpr size_t lds = sizeof(bf16bits) * kOrthParts<T> * 16 * (W / H > NT ? W / H : NT) * (16 * NT + 24);
+    constexpr size_t lds = sizeof(bf16bits) * kOrthParts<T> * 16 * W * (16 * NT + 24);
     if (lds > 64 * 1024) {
-        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_strip_kernel<T, NT, W, H>),
+        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_strip_kernel<T, NT, W>),
                                                         hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL((orth_strip_kernel<T, NT, W, H>), dim3(static_cast<unsigned>(s.o.B) * s.strips), dim3(64 * W), lds,
+    hipLaunchKernelGGL((orth_strip_kernel<T, NT, W>), dim3(static_cast<unsigned>(s.o.B) * s.strips), dim3(64 * W), lds,
                        stream, s);
     return hipGetLastError();
 }
@@ -685,10 +668,7 @@ static hipError_t strips_by_shape(const StripArgs &s, const OrthCut &c, hipStrea
     case 28: return launch_strips<T, 2, 8>(s, stream);
     case 44: return launch_strips<T, 4, 4>(s, stream);
     case 48: return launch_strips<T, 4, 8>(s, stream);
-    default:
-        return c.h == 4   ? launch_strips<T, 8, 8, 4>(s, stream)
-               : c.h == 2 ? launch_strips<T, 8, 8, 2>(s, stream)
-                          : launch_strips<T, 8, 8>(s, stream);
+    default: return launch_strips<T, 8, 8>(s, stream);
     }
 }
 

@@ -14,7 +14,8 @@ import ctypes
 
 import torch
 
-from .etp import (ETP_BF16, ETP_F32, ETP_FLAG_ACCUMULATE, EtpError, _check, _ptr, _stream, lib)  # noqa: F401
+from .etp import (ETP_BF16, ETP_F32, ETP_FLAG_ACCUMULATE, EtpError, _check, lib)  # noqa: F401
+from .etp import _stream as _any_stream
 
 ETP_ACT_NONE, ETP_ACT_SILU, ETP_ACT_GELU = 0, 1, 2
 
@@ -52,6 +53,17 @@ def _code(dtype) -> int:
     return _CODE[dtype]
 
 
+# torch's current stream of a device as a plain handle: the stream object that
+# torch.cuda.current_stream builds takes longer than all the other marshalling
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, x):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(x.get_device())
+    return _any_stream(stream)
+
+
 def _rows(t, name, dtype, rows, cols, optional=False):
     """(device pointer, row pitch) of a [rows][cols] tensor with unit column stride."""
     if t is None:
@@ -65,13 +77,30 @@ def _rows(t, name, dtype, rows, cols, optional=False):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     pitch, unit = t.stride()
-    if cols > 1 and unit != 1 or rows > 1 and pitch < cols:
+    if rows < 2:
+        pitch = cols
+    if cols > 1 and unit != 1 or pitch < cols:
         raise ValueError(f"{name} must have unit column stride and rows that do not overlap, got strides {t.stride()}")
-    return t.data_ptr(), max(pitch, cols) if rows > 1 else cols
+    return t.data_ptr(), pitch
+
+
+def _dense(t, name, dtype, numel, optional=False):
+    """Device pointer of a contiguous tensor of numel elements (None -> NULL if optional)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and have {numel} elements, got {list(t.shape)}, strides {t.stride()}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.data_ptr()
 
 
 def _workspace(ws):
-    return (None, 0) if ws is None else (_ptr(ws, "ws"), ws.numel() * ws.element_size())
+    return (None, 0) if ws is None else (_dense(ws, "ws", ws.dtype, ws.numel()), ws.numel() * ws.element_size())
 
 
 def _bytes(name, *args) -> int:
@@ -96,9 +125,9 @@ def etp_linear(x, W, y, bias=None, activation: int = ETP_ACT_NONE, residual=None
     rp, ldr = _rows(residual, "residual", dt, M, N, True)
     yp, ldy = _rows(y, "y", dt, M, N)
     zp, ldz = _rows(z, "z", dt, M, N, True)
-    _check(lib.etp_linear(M, K, N, code, xp, ldx, _ptr(W, "W", dt, K * N),
-                          _ptr(bias, "bias", torch.float32, N, optional=True), activation, rp, ldr, yp, ldy, zp, ldz,
-                          _stream(stream)), "etp_linear")
+    _check(lib.etp_linear(M, K, N, code, xp, ldx, _dense(W, "W", dt, K * N),
+                          _dense(bias, "bias", torch.float32, N, True), activation, rp, ldr, yp, ldy, zp, ldz,
+                          _stream(stream, x)), "etp_linear")
 
 
 def etp_linear_vjp_workspace(n_rows: int, n_in: int, n_out: int, dtype=torch.float32) -> int:
@@ -118,9 +147,9 @@ def etp_linear_vjp(x, W, grad_y, z=None, activation: int = ETP_ACT_NONE, grad_x=
     op, ldo = _rows(grad_x, "grad_x", dt, M, K, True)
     wp, wb = _workspace(ws)
     f32 = torch.float32
-    _check(lib.etp_linear_vjp(M, K, N, code, xp, ldx, _ptr(W, "W", dt, K * N), zp, ldz, activation, gp, ldg, op, ldo,
-                              _ptr(grad_W, "grad_W", f32, K * N, optional=True),
-                              _ptr(grad_b, "grad_b", f32, N, optional=True), flags, wp, wb, _stream(stream)),
+    _check(lib.etp_linear_vjp(M, K, N, code, xp, ldx, _dense(W, "W", dt, K * N), zp, ldz, activation, gp, ldg, op, ldo,
+                              _dense(grad_W, "grad_W", f32, K * N, True),
+                              _dense(grad_b, "grad_b", f32, N, True), flags, wp, wb, _stream(stream, grad_y)),
            "etp_linear_vjp")
 
 
@@ -132,10 +161,10 @@ def etp_layer_norm(x, y, gamma=None, beta=None, eps: float = 1e-5, mean=None, rs
     code = _code(dt)
     xp, ldx = _rows(x, "x", dt, M, C)
     yp, ldy = _rows(y, "y", dt, M, C)
-    _check(lib.etp_layer_norm(M, C, code, xp, ldx, _ptr(gamma, "gamma", f32, C, optional=True),
-                              _ptr(beta, "beta", f32, C, optional=True), eps, yp, ldy,
-                              _ptr(mean, "mean", f32, M, optional=True), _ptr(rstd, "rstd", f32, M, optional=True),
-                              _stream(stream)), "etp_layer_norm")
+    _check(lib.etp_layer_norm(M, C, code, xp, ldx, _dense(gamma, "gamma", f32, C, True),
+                              _dense(beta, "beta", f32, C, True), eps, yp, ldy,
+                              _dense(mean, "mean", f32, M, True), _dense(rstd, "rstd", f32, M, True),
+                              _stream(stream, x)), "etp_layer_norm")
 
 
 def etp_layer_norm_vjp_workspace(n_rows: int, n_cols: int, dtype=torch.float32) -> int:
@@ -153,11 +182,11 @@ def etp_layer_norm_vjp(x, mean, rstd, grad_y, gamma=None, grad_x=None, grad_gamm
     gp, ldg = _rows(grad_y, "grad_y", dt, M, C)
     op, ldo = _rows(grad_x, "grad_x", dt, M, C, True)
     wp, wb = _workspace(ws)
-    _check(lib.etp_layer_norm_vjp(M, C, code, xp, ldx, _ptr(gamma, "gamma", f32, C, optional=True),
-                                  _ptr(mean, "mean", f32, M), _ptr(rstd, "rstd", f32, M), gp, ldg, op, ldo,
-                                  _ptr(grad_gamma, "grad_gamma", f32, C, optional=True),
-                                  _ptr(grad_beta, "grad_beta", f32, C, optional=True), flags, wp, wb,
-                                  _stream(stream)), "etp_layer_norm_vjp")
+    _check(lib.etp_layer_norm_vjp(M, C, code, xp, ldx, _dense(gamma, "gamma", f32, C, True),
+                                  _dense(mean, "mean", f32, M), _dense(rstd, "rstd", f32, M), gp, ldg, op, ldo,
+                                  _dense(grad_gamma, "grad_gamma", f32, C, True),
+                                  _dense(grad_beta, "grad_beta", f32, C, True), flags, wp, wb,
+                                  _stream(stream, x)), "etp_layer_norm_vjp")
 
 
 def etp_orthogonalize_workspace(n_mats: int, rows: int, cols: int, dtype=torch.float32) -> int:
@@ -174,5 +203,5 @@ def etp_orthogonalize(G, X, steps: int = 5, coef=None, eps: float = 1e-7, ws=Non
     code = _code(dt)
     wp, wb = _workspace(ws)
     c = None if coef is None else (ctypes.c_float * 3)(*coef)
-    _check(lib.etp_orthogonalize(n, G.shape[-2], G.shape[-1], code, _ptr(G, "G", dt), steps, c, eps,
-                                 _ptr(X, "X", dt, G.numel()), wp, wb, _stream(stream)), "etp_orthogonalize")
+    _check(lib.etp_orthogonalize(n, G.shape[-2], G.shape[-1], code, _dense(G, "G", dt, G.numel()), steps, c, eps,
+                                 _dense(X, "X", dt, G.numel()), wp, wb, _stream(stream, G)), "etp_orthogonalize")
