@@ -205,8 +205,13 @@ __global__ void __launch_bounds__(64 * kVjpWaves) layer_norm_vjp_kernel(const No
         nmean = a.mean[rc];
         nrstd = a.rstd[rc];
     };
-    fetch(r);
+    // 32 floats a lane leave no registers for a row ahead
+    constexpr bool kAhead = !(sizeof(T) == 4 && NI == 8);
+    if (kAhead)
+        fetch(r);
     for (int64_t r0 = r - lane / LPR; r0 < a.M; r0 += step, r += step) {
+        if (!kAhead)
+            fetch(r);
         float h[NI][V], g[NI][V];
         const float mean = nmean, rstd = nrstd;
         const bool live = r < a.M;
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(64 * kVjpWaves) layer_norm_vjp_kernel(const No
                 g[n][i] = own ? ng[n].get(i) : 0.f;
                 h[n][i] = own ? (nx[n].get(i) - mean) * rstd : 0.f;
             }
-        if (r0 + step < a.M)
+        if (kAhead && r0 + step < a.M)
             fetch(r + step);
 #pragma unroll
         for (int n = 0; n < NI; ++n)

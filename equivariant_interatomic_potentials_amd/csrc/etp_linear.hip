@@ -368,32 +368,69 @@ __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs
     }
 }
 
-// Longer contractions: a workgroup of four waves owns 64 RT rows and 128
-// columns; the matrix goes through LDS in chunks of 32 SUB of the contraction
-// (double-buffered, one barrier a chunk), the rows through registers. RT = 2
-// halves the LDS reads and the staging per row; RT = 1 is for grids that
-// would leave compute units without work.
+// Sixteen bytes of a row operand's source as loaded, and into LDS as parts.
+template <typename T, Dense D>
+struct RowPiece {
+    using Src = std::conditional_t<D == Dense::GxD, float, T>;
+    static constexpr int V = kVec<Src>;
+    RawVec<Src> v;
+    RawVec<T> z;  // Gx
+    __device__ __forceinline__ void load(const ProductArgs &a, int64_t row, int k)
+    {
+        const int valid = a.KD - k;
+        v.load(static_cast<const Src *>(a.A) + row * a.lda + k, valid);
+        if (D == Dense::Gx && a.act != kActNone)
+            z.load(static_cast<const T *>(a.Z) + row * a.ldz + k, valid);
+    }
+    __device__ __forceinline__ void store(const ProductArgs &a, bf16bits *at, int plane) const
+    {
+        if constexpr (sizeof(Src) == 2 && D == Dense::Fwd) {
+            *reinterpret_cast<u32x4 *>(at) = v.v;
+        } else {
+            float f[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                f[i] = v.get(i);
+                if (D == Dense::Gx && a.act != kActNone)
+                    f[i] *= act_slope(a.act, z.get(i));
+            }
+            put_parts<kRowParts<T, D>>(at, plane, f);
+        }
+    }
+};
+
+// Longer contractions: a workgroup of four waves (2 x 2) owns 32 RT rows and
+// 128 columns and takes the contraction in chunks of 64 (32 for float), rows
+// and matrix through LDS: whole rows per wave on the way in (a wave that loads
+// 16 rows of 64 bytes each takes about three times as long as for 1 KiB
+// without a gap), and each operand's parts formed once. One chunk lies in LDS
+// while the next is on its way in registers; the workgroups that share a
+// compute unit fill each other's barriers. RT = 2 is for grids that would
+// leave compute units without work.
 template <typename T, Dense D, int RT>
-__global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a, const int ncol)
+__global__ void __launch_bounds__(256, 2) product_stream_kernel(const ProductArgs a, const int ncol)
 {
     using Mx = MatrixLds<T, D>;
-    constexpr int SUB = sizeof(T) == 4 ? 1 : 2, NT = 8, kCols = 128;
-    constexpr int kItems = Mx::pieces(kCols) / 256;  // per thread and chunk of 32
-    __shared__ __attribute__((aligned(16))) bf16bits matrix[2][SUB][Mx::chunk(kCols)];
+    using Piece = RowPiece<T, D>;
+    constexpr int PR = kRowParts<T, D>, SUB = sizeof(T) == 4 ? 1 : 2, kCols = 128, kRows = 32 * RT;
+    constexpr int SR = 32 * SUB + 8, kPlane = kRows * SR;  // LDS rows (elements), a part
+    constexpr int kItems = Mx::pieces(kCols) / 256;        // matrix pieces per thread and 32 of the contraction
+    constexpr int RP = 32 * SUB / Piece::V, kRowItems = kRows * RP / 256;  // pieces of a row; per thread
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    bf16bits *rows = reinterpret_cast<bf16bits *>(smem), *matrix = rows + PR * kPlane;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
     // the column blocks of a row block run side by side on one XCD
     const int b8 = blockIdx.x >> 3;
-    const int64_t rb = static_cast<int64_t>(b8 / ncol) * 8 + (blockIdx.x & 7);
-    const int64_t row0 = (rb * 4 + wave) * 16 * RT;
-    if (rb * 64 * RT >= a.M)
+    const int64_t row0 = (static_cast<int64_t>(b8 / ncol) * 8 + (blockIdx.x & 7)) * kRows;
+    if (row0 >= a.M)
         return;  // the whole workgroup
-    const int n0 = (b8 % ncol) * kCols;
+    const int n0 = (b8 % ncol) * kCols, wr = (wave >> 1) * 16 * RT, wt = (wave & 1) * 4;  // this wave's rows, tiles
 
-    f32x4 acc[NT][RT];
+    f32x4 acc[4][RT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int j = n0 + col_of_quarter<T>(t, q);
+    for (int t = 0; t < 4; ++t) {
+        const int j = n0 + col_of_quarter<T>(wt + t, q);
         f32x4 b = {0.f, 0.f, 0.f, 0.f};
         if (D == Dense::Fwd && a.bias) {
 #pragma unroll
@@ -405,62 +442,66 @@ __global__ void __launch_bounds__(256) product_stream_kernel(const ProductArgs a
             acc[t][r] = b;
     }
     const int nk = (a.KD + 32 * SUB - 1) / (32 * SUB);
-    RowChunk<T, D> xn[RT][SUB];
+    Piece xn[kRowItems];
     Raw8<T> wn[SUB][kItems];
     auto fetch = [&](int it) {
+#pragma unroll
+        for (int n = 0; n < kRowItems; ++n) {
+            const int i = threadIdx.x + 256 * n;
+            const int64_t row = row0 + i / RP;
+            xn[n].load(a, row < a.M ? row : a.M - 1, it * 32 * SUB + i % RP * Piece::V);
+        }
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int n = 0; n < kItems; ++n)
                 Mx::load(a, threadIdx.x + 256 * n, kCols, (it * SUB + u) * 32, n0, wn[u][n]);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int64_t row = row0 + 16 * r + c, rc = row < a.M ? row : a.M - 1;
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-                xn[r][u].load(a, rc, it * 32 * SUB + 32 * u + 8 * q);
-        }
     };
     fetch(0);
     for (int it = 0; it < nk; ++it) {
-        const int buf = it & 1;
+        if (it > 0)
+            lds_barrier();  // the last chunk has been read
+#pragma unroll
+        for (int n = 0; n < kRowItems; ++n) {
+            const int i = threadIdx.x + 256 * n;
+            xn[n].store(a, rows + i / RP * SR + i % RP * Piece::V, kPlane);
+        }
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int n = 0; n < kItems; ++n)
-                Mx::store(matrix[buf][u], threadIdx.x + 256 * n, kCols, wn[u][n]);
-        Frag<kRowParts<T, D>> xf[SUB][RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-                xf[u][r] = xn[r][u].frag(a);
-        // one barrier a chunk: the stores above are seen by every wave, and
-        // the buffer written next was last read before it
-        lds_barrier();
+                Mx::store(matrix + u * Mx::chunk(kCols), threadIdx.x + 256 * n, kCols, wn[u][n]);
         if (it + 1 < nk)
             fetch(it + 1);
+        lds_barrier();
 #pragma unroll
-        for (int u = 0; u < SUB; ++u)
+        for (int u = 0; u < SUB; ++u) {
+            Frag<PR> xf[RT];
 #pragma unroll
-            for (int t = 0; t < NT; t += 2) {
-                const Frag<kParts<T>> w[2] = {Mx::tile(matrix[buf][u], t, kCols, lane),
-                                              Mx::tile(matrix[buf][u], t + 1, kCols, lane)};
-                mma(w, xf[u], acc, t);
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int p = 0; p < PR; ++p)
+                    xf[r].p[p] =
+                        *reinterpret_cast<const bf16x8 *>(rows + p * kPlane + (wr + 16 * r + c) * SR + 32 * u + 8 * q);
+#pragma unroll
+            for (int t = 0; t < 4; t += 2) {
+                const bf16bits *m = matrix + u * Mx::chunk(kCols);
+                const Frag<kParts<T>> w[2] = {Mx::tile(m, wt + t, kCols, lane), Mx::tile(m, wt + t + 1, kCols, lane)};
+                mma(w, xf, acc, t);
             }
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            if (n0 + 64 * g >= a.ND)
-                break;
-            const int64_t row = row0 + 16 * r + c;
-            float add[sizeof(T) == 4 ? 4 : 2][8];
-            load_group_addend<T, D>(a, row, n0 + 64 * g, q, add);
-            const f32x4 v[4][1] = {{acc[4 * g][r]}, {acc[4 * g + 1][r]}, {acc[4 * g + 2][r]}, {acc[4 * g + 3][r]}};
-            store_group<T, D>(a, row, n0 + 64 * g, q, v, add);
         }
+    }
+    const int j0 = n0 + 16 * wt;
+    if (j0 >= a.ND)
+        return;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int64_t row = row0 + wr + 16 * r + c;
+        float add[sizeof(T) == 4 ? 4 : 2][8];
+        load_group_addend<T, D>(a, row, j0, q, add);
+        const f32x4 v[4][1] = {{acc[0][r]}, {acc[1][r]}, {acc[2][r]}, {acc[3][r]}};
+        store_group<T, D>(a, row, j0, q, v, add);
+    }
 }
 
 // Few rows and a long contraction: a workgroup owns 16 rows and 64 columns,
@@ -535,6 +576,18 @@ static hipError_t launch_resident(const ProductArgs &a, dim3 grid, dim3 block, s
     return hipGetLastError();
 }
 
+template <typename T, Dense D, int RT>
+static hipError_t launch_stream(const ProductArgs &a, int ncol, hipStream_t stream)
+{
+    constexpr int SUB = sizeof(T) == 4 ? 1 : 2;
+    constexpr size_t lds = sizeof(bf16bits) * (kRowParts<T, D> * 32 * RT * (32 * SUB + 8) + SUB * MatrixLds<T, D>::chunk(128));
+    static_assert(lds <= 64 * 1024);
+    const int64_t blocks = (a.M + 32 * RT - 1) / (32 * RT);
+    hipLaunchKernelGGL((product_stream_kernel<T, D, RT>), dim3(static_cast<unsigned>((blocks + 7) / 8 * 8 * ncol)),
+                       dim3(256), lds, stream, a, ncol);
+    return hipGetLastError();
+}
+
 template <typename T, Dense D>
 static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
 {
@@ -563,16 +616,9 @@ static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
         const int nc = (a.ND + 63) / 64;
         hipLaunchKernelGGL((product_thin_kernel<T, D>), dim3(static_cast<unsigned>(ntile * nc)), dim3(256), 0, stream,
                            a, nc);
-    } else if (wide < 2 * kComputeUnits) {
-        hipLaunchKernelGGL((product_stream_kernel<T, D, 1>),
-                           dim3(static_cast<unsigned>(((a.M + 63) / 64 + 7) / 8 * 8 * ncol)), dim3(256), 0, stream, a,
-                           ncol);
-    } else {
-        hipLaunchKernelGGL((product_stream_kernel<T, D, 2>),
-                           dim3(static_cast<unsigned>(((a.M + 127) / 128 + 7) / 8 * 8 * ncol)), dim3(256), 0, stream,
-                           a, ncol);
+        return hipGetLastError();
     }
-    return hipGetLastError();
+    return wide < 2 * kComputeUnits ? launch_stream<T, D, 2>(a, ncol, stream) : launch_stream<T, D, 4>(a, ncol, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -606,7 +652,7 @@ struct PanelArgs {
 struct PanelShape {
     int px, waves, sx, sd, bufs, rows, lds, per_cu;  // parts of x, row strides (elements), workgroups that fit
     constexpr PanelShape(bool bf16, int kc, int nc)
-        : px(bf16 ? 1 : 3), waves(kc == 4 || nc == 4 ? 8 : 4), sx(32 * kc + 8), sd(32 * nc + 8),
+        : px(bf16 ? 1 : 3), waves(bf16 ? (kc == 4 && nc > 1 ? 8 : 4) : (kc == 4 || nc == 4 ? 8 : 4)), sx(32 * kc + 8), sd(32 * nc + 8),
           bufs(waves == 8 ? 2 : 1), rows(2 * bufs * 64 * (px * sx + 3 * sd) <= 144 * 1024 ? 64 : 32),
           lds(2 * bufs * rows * (px * sx + 3 * sd)),
           per_cu(waves == 8 ? 1 : 160 * 1024 / lds < 3 ? 160 * 1024 / lds : 3)
@@ -950,9 +996,11 @@ hipError_t launch_linear(const LinearArgs &a, hipStream_t stream)
 }
 
 // How a VJP call is cut: all in one panel kernel where K and N are at most
-// 128, else d once, gx as a product and gW in blocks.
+// 128, else gx as a product and gW in blocks of up to 128 x 128, with d made
+// once before both where K and N are above 128 (where only one is, forming d
+// again costs less than keeping it).
 struct VjpCut {
-    bool fused;
+    bool fused, keep_d;  // one kernel for all; d made once
     int kc, nc;          // chunks of 32 of a block: 1, 2 or 4
     int nkb, nnb;        // blocks along K and N
     int64_t npanel;
@@ -969,13 +1017,14 @@ static VjpCut vjp_cut(int64_t M, int K, int N, bool bf16)
     v.nkb = (K + 127) / 128;
     v.nnb = (N + 127) / 128;
     v.fused = K <= 128 && N <= 128;
-    const PanelShape shape(bf16, v.fused ? v.kc : 4, v.fused ? v.nc : 4);
+    const PanelShape shape(bf16, v.kc, v.nc);
     v.npanel = (M + shape.rows - 1) / shape.rows;
     const int64_t blocks = static_cast<int64_t>(v.nkb) * v.nnb;
     int64_t s = (static_cast<int64_t>(kComputeUnits) * shape.per_cu + blocks - 1) / blocks;
     s = s < v.npanel ? s : v.npanel;
     v.nsplit = static_cast<int>(s < 1 ? 1 : s);
-    v.d_bytes = v.fused ? 0 : (sizeof(float) * static_cast<size_t>(M) * N + 15) / 16 * 16;
+    v.keep_d = K > 128 && N > 128;
+    v.d_bytes = v.keep_d ? (sizeof(float) * static_cast<size_t>(M) * N + 15) / 16 * 16 : 0;
     v.part_bytes = sizeof(float) * static_cast<size_t>(v.nsplit) * (static_cast<size_t>(K) + 1) * N;
     return v;
 }
@@ -1007,19 +1056,19 @@ static hipError_t launch_panel(const PanelArgs &p, int blocks, hipStream_t strea
 template <typename T>
 static hipError_t panel_by_shape(const PanelArgs &p, const VjpCut &v, hipStream_t stream)
 {
-    if (!v.fused)
-        return p.d ? launch_panel<T, 4, 4, true>(p, v.nkb * v.nnb, stream)
-                   : launch_panel<T, 4, 4, false>(p, v.nkb * v.nnb, stream);
+    if (p.d)
+        return launch_panel<T, 4, 4, true>(p, v.nkb * v.nnb, stream);
+    const int blocks = v.nkb * v.nnb;
     switch (v.kc * 8 + v.nc) {
-    case 9: return launch_panel<T, 1, 1, false>(p, 1, stream);
-    case 10: return launch_panel<T, 1, 2, false>(p, 1, stream);
-    case 12: return launch_panel<T, 1, 4, false>(p, 1, stream);
-    case 17: return launch_panel<T, 2, 1, false>(p, 1, stream);
-    case 18: return launch_panel<T, 2, 2, false>(p, 1, stream);
-    case 20: return launch_panel<T, 2, 4, false>(p, 1, stream);
-    case 33: return launch_panel<T, 4, 1, false>(p, 1, stream);
-    case 34: return launch_panel<T, 4, 2, false>(p, 1, stream);
-    default: return launch_panel<T, 4, 4, false>(p, 1, stream);
+    case 9: return launch_panel<T, 1, 1, false>(p, blocks, stream);
+    case 10: return launch_panel<T, 1, 2, false>(p, blocks, stream);
+    case 12: return launch_panel<T, 1, 4, false>(p, blocks, stream);
+    case 17: return launch_panel<T, 2, 1, false>(p, blocks, stream);
+    case 18: return launch_panel<T, 2, 2, false>(p, blocks, stream);
+    case 20: return launch_panel<T, 2, 4, false>(p, blocks, stream);
+    case 33: return launch_panel<T, 4, 1, false>(p, blocks, stream);
+    case 34: return launch_panel<T, 4, 2, false>(p, blocks, stream);
+    default: return launch_panel<T, 4, 4, false>(p, blocks, stream);
     }
 }
 
@@ -1032,7 +1081,7 @@ static hipError_t linear_vjp(const LinearVjpArgs &a, hipStream_t stream)
     hipError_t e = hipSuccess;
     if (!v.fused || !sums) {
         // without the sums there is no workspace either: d as the product goes
-        if (sums && a.act != kActNone) {
+        if (sums && v.keep_d && a.act != kActNone) {
             float *d = reinterpret_cast<float *>(static_cast<unsigned char *>(a.ws) + v.part_bytes);
             const int64_t blocks = (a.M * ((a.N + 7) / 8) + 255) / 256;
             hipLaunchKernelGGL(slope_kernel<T>, dim3(static_cast<unsigned>(blocks < 16384 ? blocks : 16384)),
