@@ -605,8 +605,10 @@ static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
         const int per_cu = static_cast<int>(160 * 1024 / lds) < 16 / waves ? static_cast<int>(160 * 1024 / lds)
                                                                             : 16 / waves;
         int64_t streams = (ntile + waves - 1) / waves;
-        const int64_t most = (static_cast<int64_t>(kComputeUnits) * per_cu + nsplit - 1) / nsplit;
-        streams = ((streams < most ? streams : most) + 7) / 8 * 8;
+        // no more than run at once, in eighths of the chip
+        const int64_t most = kComputeUnits * per_cu / nsplit / 8 * 8;
+        streams = (streams + 7) / 8 * 8;
+        streams = streams < most ? streams : most < 8 ? 8 : most;
         const dim3 grid(static_cast<unsigned>(streams * nsplit)), block(64 * waves);
         switch (kc) {
         case 1: return launch_resident<T, D, 1>(a, grid, block, lds, nb, nsplit, stream);
@@ -647,6 +649,7 @@ struct PanelArgs {
     int64_t npanel;
     int nsplit;       // workgroups along the panels
     int nkb;          // blocks of 32 KC along K (1 with gx)
+    int blocks;       // of gW
 };
 
 // With eight waves and one workgroup a compute unit, two panels' parts lie in
@@ -680,7 +683,16 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
     const LinearVjpArgs &a = p.v;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int s = blockIdx.x % p.nsplit, blk = blockIdx.x / p.nsplit;
+    // workgroup i runs on XCD i % 8: the blocks that read the same panels run
+    // on one of them, so that its L2 serves all but the first (20000 x 384 x
+    // 1024 bf16, with the splits cut to one round: 202 -> 155 us). A single
+    // block has nothing to share and walks in step (5172508 x 64 x 64 bf16:
+    // 535 us, 549 by XCD).
+    const int total = p.nsplit * p.blocks, each = (total + 7) / 8;
+    const int id = p.blocks > 1 ? (blockIdx.x & 7) * each + (blockIdx.x >> 3) : blockIdx.x;
+    if (id >= total)
+        return;
+    const int s = id / p.blocks, blk = id % p.blocks;
     const int k0 = (blk % p.nkb) * 32 * KC, j0 = (blk / p.nkb) * 32 * NC;
     const int K = a.K, N = a.N;
     const bool want_gx = a.gx != nullptr, want_gw = a.gW != nullptr, want_gb = a.gb != nullptr && k0 == 0;
@@ -1025,8 +1037,17 @@ static VjpCut vjp_cut(int64_t M, int K, int N, bool bf16)
     v.fused = K <= 128 && N <= 128;
     const PanelShape shape(bf16, v.kc, v.nc);
     v.npanel = (M + shape.rows - 1) / shape.rows;
-    const int64_t blocks = static_cast<int64_t>(v.nkb) * v.nnb;
-    int64_t s = (static_cast<int64_t>(kComputeUnits) * shape.per_cu + blocks - 1) / blocks;
+    // as many splits as run at once (one more would double the time), or over
+    // up to four rounds where that fills them better by a tenth
+    const int64_t blocks = static_cast<int64_t>(v.nkb) * v.nnb, room = static_cast<int64_t>(kComputeUnits) * shape.per_cu;
+    int64_t s = 0, rounds = 1;
+    for (int64_t n = 1; n <= 4; ++n) {
+        const int64_t t = n * room / blocks;
+        if (s == 0 ? t > 0 : 10 * n * s < 9 * rounds * t) {
+            s = t;
+            rounds = n;
+        }
+    }
     s = s < v.npanel ? s : v.npanel;
     v.nsplit = static_cast<int>(s < 1 ? 1 : s);
     v.keep_d = K > 128 && N > 128;
@@ -1044,7 +1065,7 @@ size_t linear_vjp_workspace_bytes(int64_t M, int K, int N, bool bf16)
 }
 
 template <typename T, int KC, int NC, bool FromD>
-static hipError_t launch_panel(const PanelArgs &p, int blocks, hipStream_t stream)
+static hipError_t launch_panel(const PanelArgs &p, hipStream_t stream)
 {
     constexpr PanelShape S = kPanelShape<T, KC, NC>;
     if (S.lds > 64 * 1024) {
@@ -1054,7 +1075,7 @@ static hipError_t launch_panel(const PanelArgs &p, int blocks, hipStream_t strea
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL((panel_kernel<T, KC, NC, FromD>), dim3(static_cast<unsigned>(p.nsplit * blocks)),
+    hipLaunchKernelGGL((panel_kernel<T, KC, NC, FromD>), dim3(static_cast<unsigned>((p.nsplit * p.blocks + 7) / 8 * 8)),
                        dim3(64 * S.waves), S.lds, stream, p);
     return hipGetLastError();
 }
@@ -1063,18 +1084,17 @@ template <typename T>
 static hipError_t panel_by_shape(const PanelArgs &p, const VjpCut &v, hipStream_t stream)
 {
     if (p.d)
-        return launch_panel<T, 4, 4, true>(p, v.nkb * v.nnb, stream);
-    const int blocks = v.nkb * v.nnb;
+        return launch_panel<T, 4, 4, true>(p, stream);
     switch (v.kc * 8 + v.nc) {
-    case 9: return launch_panel<T, 1, 1, false>(p, blocks, stream);
-    case 10: return launch_panel<T, 1, 2, false>(p, blocks, stream);
-    case 12: return launch_panel<T, 1, 4, false>(p, blocks, stream);
-    case 17: return launch_panel<T, 2, 1, false>(p, blocks, stream);
-    case 18: return launch_panel<T, 2, 2, false>(p, blocks, stream);
-    case 20: return launch_panel<T, 2, 4, false>(p, blocks, stream);
-    case 33: return launch_panel<T, 4, 1, false>(p, blocks, stream);
-    case 34: return launch_panel<T, 4, 2, false>(p, blocks, stream);
-    default: return launch_panel<T, 4, 4, false>(p, blocks, stream);
+    case 9: return launch_panel<T, 1, 1, false>(p, stream);
+    case 10: return launch_panel<T, 1, 2, false>(p, stream);
+    case 12: return launch_panel<T, 1, 4, false>(p, stream);
+    case 17: return launch_panel<T, 2, 1, false>(p, stream);
+    case 18: return launch_panel<T, 2, 2, false>(p, stream);
+    case 20: return launch_panel<T, 2, 4, false>(p, stream);
+    case 33: return launch_panel<T, 4, 1, false>(p, stream);
+    case 34: return launch_panel<T, 4, 2, false>(p, stream);
+    default: return launch_panel<T, 4, 4, false>(p, stream);
     }
 }
 
@@ -1083,7 +1103,7 @@ static hipError_t linear_vjp(const LinearVjpArgs &a, hipStream_t stream)
 {
     const bool sums = a.gW || a.gb;
     const VjpCut v = vjp_cut(a.M, a.K, a.N, a.bf16);
-    PanelArgs p{a, nullptr, v.npanel, v.nsplit, v.nkb};
+    PanelArgs p{a, nullptr, v.npanel, v.nsplit, v.nkb, v.nkb * v.nnb};
     hipError_t e = hipSuccess;
     if (!v.fused || !sums) {
         // without the sums there is no workspace either: d as the product goes
