@@ -61,9 +61,8 @@ __device__ __forceinline__ Frag<P> split8(const float (&v)[8])
     return f;
 }
 
-// A workgroup barrier for what goes through LDS: it waits for this wave's LDS
-// accesses, and not, as __syncthreads does, for its loads from memory, so that
-// what was asked for ahead stays in flight across it.
+// A workgroup barrier for what goes through LDS: it orders LDS accesses only,
+// so that loads from memory that were asked for ahead stay in flight across it.
 __device__ __forceinline__ void lds_barrier()
 {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");

@@ -10,6 +10,11 @@
 // stride and load the next row while they work on the present one. Rows of
 // more than 2048 columns take a workgroup each and read the row again (from
 // cache) for every sum.
+//
+// Measured: forward 32768 x 512 bf16 12.4 us (5.4 TB/s, part of it from
+// cache); VJP 441172 x 64 float 66 us (5.2 TB/s), 5184 x 777 bf16 16 us (1.5
+// TB/s: two launches, and rows of 1554 bytes on any alignment), 50000 x 2000
+// float 240 us (5.0 TB/s).
 #include "etp_dense_mma.hpp"
 
 namespace etp {

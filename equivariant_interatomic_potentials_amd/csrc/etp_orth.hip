@@ -15,11 +15,16 @@
 //    strip of X stays in registers for all steps (a wave holds 16 columns, all
 //    n rows, in accumulator layout, which is also the operand layout of P X);
 //    LDS holds the parts of X^T, then of A, then of P in the same space. With
-//    one strip (m <= 128) all steps are one launch. Wider matrices take one
+//    one strip (m <= 128) all steps are one launch: a matrix has one compute
+//    unit, whose matrix instructions are busy 42% of the time and wait for LDS
+//    otherwise (34 of 128 x 128 float: 73 us, five steps; spread over more
+//    units with a launch a step: 87). Wider matrices take one
 //    launch per step: each strip adds the strips' partial A in order, forms P
 //    for itself, updates its columns and leaves its part of the next A.
 //  * larger: three products a step over the parts in global memory, 64 x 64
-//    tiles (orth_product_kernel).
+//    tiles (orth_product_kernel). 15 launches that wait for each other, each of
+//    8 to 12 us, of which a unit's loads at 64 bytes a cycle are half (two of
+//    512 x 1024 bf16: 155 us).
 #include <type_traits>
 
 #include "etp_dense_mma.hpp"
@@ -132,7 +137,8 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
     __shared__ double red[W];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int b = blockIdx.x / s.strips, g = blockIdx.x % s.strips;
+    const int b = blockIdx.y, g = blockIdx.x;
+    const int64_t id = static_cast<int64_t>(b) * s.strips + g;
     const int n = s.n, m = s.m, col = 16 * W * g + 16 * wave + c;
     const int64_t nm = static_cast<int64_t>(n) * m;
     const float ca = s.o.coef[0], cb = s.o.coef[1], cc = s.o.coef[2];
@@ -148,8 +154,8 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 
     // the strip: x[i][r] = X[16 i + 4 q + r][col]
     f32x4 x[NT];
-    const float *xs = s.x_in + (static_cast<int64_t>(blockIdx.x) * W + wave) * NT * 256 + lane * 4;
-    float *xs_out = s.x_out + (static_cast<int64_t>(blockIdx.x) * W + wave) * NT * 256 + lane * 4;
+    const float *xs = s.x_in + (id * W + wave) * NT * 256 + lane * 4;
+    float *xs_out = s.x_out + (id * W + wave) * NT * 256 + lane * 4;
     if (s.strips == 1 || s.step < 0) {
         const T *G = static_cast<const T *>(s.o.G) + b * nm;
 #pragma unroll
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
             }
             gram();
             if (!one) {
-                float *out = s.a_out + static_cast<int64_t>(blockIdx.x) * set + own;
+                float *out = s.a_out + id * set + own;
 #pragma unroll
                 for (int i = 0; i < OMAX; ++i)
                     *reinterpret_cast<f32x4 *>(out + i * 256) = acc[i][0];
@@ -427,9 +433,8 @@ __global__ void __launch_bounds__(256, 1) orth_product_kernel(const OrthProductA
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
     // workgroups b and b + 8 run on the same XCD: each XCD takes a run of
-    // consecutive tiles, so that it fetches few rows of the operands (every
-    // launch begins with cold caches, and an XCD gets 0.6 TB/s from beyond
-    // its own)
+    // consecutive tiles, so that it fetches few rows of the operands into its
+    // L2
     const int w = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
     if (w >= a.tiles * a.mats)
         return;  // the whole workgroup: padding to a multiple of 8
@@ -649,12 +654,12 @@ static hipError_t launch_strips(const StripArgs &s, hipStream_t stream)
 {
     constexpr size_t lds = sizeof(bf16bits) * kOrthParts<T> * 16 * W * (16 * NT + 24);
     if (lds > 64 * 1024) {
-        static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_strip_kernel<T, NT, W>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_strip_kernel<T, NT, W>),
                                                         hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL((orth_strip_kernel<T, NT, W>), dim3(static_cast<unsigned>(s.o.B) * s.strips), dim3(64 * W), lds,
+    hipLaunchKernelGGL((orth_strip_kernel<T, NT, W>), dim3(s.strips, s.o.B), dim3(64 * W), lds,
                        stream, s);
     return hipGetLastError();
 }
@@ -676,7 +681,7 @@ template <typename T, OrthOp Op>
 static hipError_t launch_orth_product(const OrthProductArgs &a, hipStream_t stream)
 {
     constexpr size_t lds = 4 * kOT * kOrthOut * sizeof(float);
-    static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_product_kernel<T, Op>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_product_kernel<T, Op>),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess)
         return e;
