@@ -416,18 +416,22 @@ struct RowPiece {
 // without a gap), and each operand's parts formed once. One chunk lies in LDS
 // while the next is on its way in registers; the workgroups that share a
 // compute unit fill each other's barriers. RT = 2 is for grids that would
-// leave compute units without work. Bound by LDS reads and matrix instructions
-// taking turns: 32768 x 512 x 512 forward float 120 us (a library's float
+// leave compute units without work. Narrow results take 64 or 32 columns, the
+// waves one below the other, where 128 would mostly multiply zeros: 441172 x
+// 256 x 8 float 176 -> 98 us, 4.9 TB/s, x 64 bf16 129 -> 78 us, 4.3 TB/s. Wide
+// ones are bound by LDS reads and matrix instructions taking turns: 32768 x 512 x 512 forward float 120 us (a library's float
 // product of that size: 115 at its best rate), bf16 47 us, input gradient from
 // a kept d 48 us.
-template <typename T, Dense D, int RT>
-__global__ void __launch_bounds__(256, 2) product_stream_kernel(const ProductArgs a, const int ncol)
+template <typename T, Dense D, int RT, int kCols>
+__global__ void __launch_bounds__(256, kCols == 128 ? 2 : kCols == 64 ? 3 : 4) product_stream_kernel(const ProductArgs a, const int ncol)
 {
     using Mx = MatrixLds<T, D>;
     using Piece = RowPiece<T, D>;
-    constexpr int PR = kRowParts<T, D>, SUB = sizeof(T) == 4 ? 1 : 2, kCols = 128, kRows = 32 * RT;
+    constexpr int PR = kRowParts<T, D>, SUB = sizeof(T) == 4 ? 1 : 2, kRows = 32 * RT;
+    constexpr int WC = kCols == 128 ? 2 : 1, RW = RT * WC / 2, TW = kCols / 16 / WC;  // waves across, a wave's tiles
     constexpr int SR = 32 * SUB + 8, kPlane = kRows * SR;  // LDS rows (elements), a part
-    constexpr int kItems = Mx::pieces(kCols) / 256;        // matrix pieces per thread and 32 of the contraction
+    constexpr int kItems = (Mx::pieces(kCols) + 255) / 256;  // matrix pieces per thread and 32 of the contraction
+    const bool lays = Mx::pieces(kCols) % 256 == 0 || threadIdx.x < Mx::pieces(kCols);
     constexpr int RP = 32 * SUB / Piece::V, kRowItems = kRows * RP / 256;  // pieces of a row; per thread
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     bf16bits *rows = reinterpret_cast<bf16bits *>(smem), *matrix = rows + PR * kPlane;
@@ -438,11 +442,11 @@ __global__ void __launch_bounds__(256, 2) product_stream_kernel(const ProductArg
     const int64_t row0 = (static_cast<int64_t>(b8 / ncol) * 8 + (blockIdx.x & 7)) * kRows;
     if (row0 >= a.M)
         return;  // the whole workgroup
-    const int n0 = (b8 % ncol) * kCols, wr = (wave >> 1) * 16 * RT, wt = (wave & 1) * 4;  // this wave's rows, tiles
+    const int n0 = (b8 % ncol) * kCols, wr = wave / WC * 16 * RW, wt = wave % WC * TW;  // this wave's rows, tiles
 
-    f32x4 acc[4][RT];
+    f32x4 acc[TW][RW];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < TW; ++t) {
         const int j = n0 + col_of_quarter<T>(wt + t, q);
         f32x4 b = {0.f, 0.f, 0.f, 0.f};
         if (D == Dense::Fwd && a.bias) {
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(256, 2) product_stream_kernel(const ProductArg
                 b[i] = j + i < a.ND ? a.bias[j + i] : 0.f;
         }
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int r = 0; r < RW; ++r)
             acc[t][r] = b;
     }
     const int nk = (a.KD + 32 * SUB - 1) / (32 * SUB);
@@ -468,7 +472,8 @@ __global__ void __launch_bounds__(256, 2) product_stream_kernel(const ProductArg
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int n = 0; n < kItems; ++n)
-                Mx::load(a, threadIdx.x + 256 * n, kCols, (it * SUB + u) * 32, n0, wn[u][n]);
+                if (lays)
+                    Mx::load(a, threadIdx.x + 256 * n, kCols, (it * SUB + u) * 32, n0, wn[u][n]);
     };
     fetch(0);
     for (int it = 0; it < nk; ++it) {
@@ -483,21 +488,22 @@ __global__ void __launch_bounds__(256, 2) product_stream_kernel(const ProductArg
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int n = 0; n < kItems; ++n)
-                Mx::store(matrix + u * Mx::chunk(kCols), threadIdx.x + 256 * n, kCols, wn[u][n]);
+                if (lays)
+                    Mx::store(matrix + u * Mx::chunk(kCols), threadIdx.x + 256 * n, kCols, wn[u][n]);
         if (it + 1 < nk)
             fetch(it + 1);
         lds_barrier();
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-            Frag<PR> xf[RT];
+            Frag<PR> xf[RW];
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < RW; ++r)
 #pragma unroll
                 for (int p = 0; p < PR; ++p)
                     xf[r].p[p] =
                         *reinterpret_cast<const bf16x8 *>(rows + p * kPlane + (wr + 16 * r + c) * SR + 32 * u + 8 * q);
 #pragma unroll
-            for (int t = 0; t < 4; t += 2) {
+            for (int t = 0; t < TW; t += 2) {
                 const bf16bits *m = matrix + u * Mx::chunk(kCols);
                 const Frag<kParts<T>> w[2] = {Mx::tile(m, wt + t, kCols, lane), Mx::tile(m, wt + t + 1, kCols, lane)};
                 mma(w, xf, acc, t);
@@ -508,11 +514,14 @@ __global__ void __launch_bounds__(256, 2) product_stream_kernel(const ProductArg
     if (j0 >= a.ND)
         return;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
+    for (int r = 0; r < RW; ++r) {
         const int64_t row = row0 + wr + 16 * r + c;
         float add[sizeof(T) == 4 ? 4 : 2][8];
         load_group_addend<T, D>(a, row, j0, q, add);
-        const f32x4 v[4][1] = {{acc[0][r]}, {acc[1][r]}, {acc[2][r]}, {acc[3][r]}};
+        f32x4 v[4][1] = {};  // 32 columns: the others are past ND
+#pragma unroll
+        for (int t = 0; t < TW; ++t)
+            v[t][0] = acc[t][r];
         store_group<T, D>(a, row, j0, q, v, add);
     }
 }
@@ -591,14 +600,14 @@ static hipError_t launch_resident(const ProductArgs &a, dim3 grid, dim3 block, s
     return hipGetLastError();
 }
 
-template <typename T, Dense D, int RT>
+template <typename T, Dense D, int RT, int kCols>
 static hipError_t launch_stream(const ProductArgs &a, int ncol, hipStream_t stream)
 {
     constexpr int SUB = sizeof(T) == 4 ? 1 : 2;
-    constexpr size_t lds = sizeof(bf16bits) * (kRowParts<T, D> * 32 * RT * (32 * SUB + 8) + SUB * MatrixLds<T, D>::chunk(128));
+    constexpr size_t lds = sizeof(bf16bits) * (kRowParts<T, D> * 32 * RT * (32 * SUB + 8) + SUB * MatrixLds<T, D>::chunk(kCols));
     static_assert(lds <= 64 * 1024);
     const int64_t blocks = (a.M + 32 * RT - 1) / (32 * RT);
-    hipLaunchKernelGGL((product_stream_kernel<T, D, RT>), dim3(static_cast<unsigned>((blocks + 7) / 8 * 8 * ncol)),
+    hipLaunchKernelGGL((product_stream_kernel<T, D, RT, kCols>), dim3(static_cast<unsigned>((blocks + 7) / 8 * 8 * ncol)),
                        dim3(256), lds, stream, a, ncol);
     return hipGetLastError();
 }
@@ -635,7 +644,16 @@ static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
                            a, nc);
         return hipGetLastError();
     }
-    return wide < 2 * kComputeUnits ? launch_stream<T, D, 2>(a, ncol, stream) : launch_stream<T, D, 4>(a, ncol, stream);
+    if constexpr (D != Dense::GxD) {  // (d is kept for wide layers only)
+        if (a.ND <= 32)
+            return wide < 2 * kComputeUnits ? launch_stream<T, D, 2, 32>(a, 1, stream)
+                                            : launch_stream<T, D, 4, 32>(a, 1, stream);
+        if (a.ND <= 64)
+            return wide < 2 * kComputeUnits ? launch_stream<T, D, 2, 64>(a, 1, stream)
+                                            : launch_stream<T, D, 4, 64>(a, 1, stream);
+    }
+    return wide < 2 * kComputeUnits ? launch_stream<T, D, 2, 128>(a, ncol, stream)
+                                    : launch_stream<T, D, 4, 128>(a, ncol, stream);
 }
 
 // ---------------------------------------------------------------------------
