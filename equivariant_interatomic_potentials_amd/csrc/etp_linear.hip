@@ -419,9 +419,9 @@ struct RowPiece {
 // leave compute units without work. Narrow results take 64 or 32 columns, the
 // waves one below the other, where 128 would mostly multiply zeros: 441172 x
 // 256 x 8 float 176 -> 98 us, 4.9 TB/s, x 64 bf16 129 -> 78 us, 4.3 TB/s. Wide
-// ones are bound by LDS reads and matrix instructions taking turns: 32768 x 512 x 512 forward float 120 us (a library's float
-// product of that size: 115 at its best rate), bf16 47 us, input gradient from
-// a kept d 48 us.
+// ones are bound by LDS reads and matrix instructions taking turns: 32768 x
+// 512 x 512 forward float 120 us (a library's float product of that size: 115
+// at its best rate), bf16 44 us, input gradient from a kept d 48 us.
 template <typename T, Dense D, int RT, int kCols>
 __global__ void __launch_bounds__(256, kCols == 128 ? 2 : kCols == 64 ? 3 : 4) product_stream_kernel(const ProductArgs a, const int ncol)
 {
