@@ -40,10 +40,18 @@ struct ProductArgs {
     bool accumulate;
 };
 
-// Parts of the row operand: a stored float exactly; d of a bf16 layer in two
-// (2^-16 relative, far below the rounding of the bf16 result).
+// Parts of the row operand, which hold it exactly: a stored value, or d, which
+// is a float also in a bf16 layer (with two of its parts terms that cancel
+// would leave grad_x wrong by up to 2^-15 of each).
 template <typename T, Dense D>
-constexpr int kRowParts = sizeof(T) == 4 ? 3 : (D == Dense::Fwd ? 1 : 2);
+constexpr int kRowParts = D == Dense::Fwd ? kParts<T> : 3;
+
+// Chunks of 32 of the contraction that a tile of a long one takes at a time:
+// two, but one where the rows have three parts, so that more workgroups share a
+// compute unit (grad_x alone, 200000 x 128 x 300 bf16: 130 us with one, 136 with
+// two; 20000 x 384 x 1024: 74 and 87).
+template <typename T, Dense D>
+constexpr int kStreamSub = kRowParts<T, D> == 3 ? 1 : 2;
 
 // Eight entries of a row as loaded, and as matrix-core parts.
 template <typename T, Dense D>
@@ -410,8 +418,8 @@ struct RowPiece {
 };
 
 // Longer contractions: a workgroup of four waves (2 x 2) owns 32 RT rows and
-// 128 columns and takes the contraction in chunks of 64 (32 for float), rows
-// and matrix through LDS: whole rows per wave on the way in (a wave that loads
+// 128 columns and takes the contraction in chunks of 64 (32 where the rows
+// have three parts), rows and matrix through LDS: whole rows per wave on the way in (a wave that loads
 // 16 rows of 64 bytes each takes about three times as long as for 1 KiB
 // without a gap), and each operand's parts formed once. One chunk lies in LDS
 // while the next is on its way in registers; the workgroups that share a
@@ -421,13 +429,13 @@ struct RowPiece {
 // 256 x 8 float 176 -> 98 us, 4.9 TB/s, x 64 bf16 129 -> 78 us, 4.3 TB/s. Wide
 // ones are bound by LDS reads and matrix instructions taking turns: 32768 x
 // 512 x 512 forward float 120 us (a library's float product of that size: 115
-// at its best rate), bf16 44 us, input gradient from a kept d 48 us.
+// at its best rate), bf16 44 us.
 template <typename T, Dense D, int RT, int kCols>
 __global__ void __launch_bounds__(256, kCols == 128 ? 2 : kCols == 64 ? 3 : 4) product_stream_kernel(const ProductArgs a, const int ncol)
 {
     using Mx = MatrixLds<T, D>;
     using Piece = RowPiece<T, D>;
-    constexpr int PR = kRowParts<T, D>, SUB = sizeof(T) == 4 ? 1 : 2, kRows = 32 * RT;
+    constexpr int PR = kRowParts<T, D>, SUB = kStreamSub<T, D>, kRows = 32 * RT;
     constexpr int WC = kCols == 128 ? 2 : 1, RW = RT * WC / 2, TW = kCols / 16 / WC;  // waves across, a wave's tiles
     constexpr int SR = 32 * SUB + 8, kPlane = kRows * SR;  // LDS rows (elements), a part
     constexpr int kItems = (Mx::pieces(kCols) + 255) / 256;  // matrix pieces per thread and 32 of the contraction
@@ -603,7 +611,7 @@ static hipError_t launch_resident(const ProductArgs &a, dim3 grid, dim3 block, s
 template <typename T, Dense D, int RT, int kCols>
 static hipError_t launch_stream(const ProductArgs &a, int ncol, hipStream_t stream)
 {
-    constexpr int SUB = sizeof(T) == 4 ? 1 : 2;
+    constexpr int SUB = kStreamSub<T, D>;
     constexpr size_t lds = sizeof(bf16bits) * (kRowParts<T, D> * 32 * RT * (32 * SUB + 8) + SUB * MatrixLds<T, D>::chunk(kCols));
     static_assert(lds <= 64 * 1024);
     const int64_t blocks = (a.M + 32 * RT - 1) / (32 * RT);
@@ -867,7 +875,6 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
                 fetch(panel + 2 * p.nsplit);
         }
         if (gx_wave) {
-            constexpr int PD = sizeof(T) == 4 ? 3 : 2;  // parts of d that a bf16 gx needs
             f32x4 o[G][RT];
 #pragma unroll
             for (int g = 0; g < G; ++g)
@@ -876,11 +883,11 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
                     o[g][r] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
-                Frag<PD> df[RT];
+                Frag<3> df[RT];
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
-                    for (int t = 0; t < PD; ++t)
+                    for (int t = 0; t < 3; ++t)
                         df[r].p[t] = *reinterpret_cast<const bf16x8 *>(
                             dl + (t * kRows + 16 * (rt0 + r) + c) * SD + 32 * n + 8 * q);
                 mma(wf[n], df, o);

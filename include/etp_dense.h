@@ -27,9 +27,8 @@
  *     are added in float: relative error per product below 2^-22, as a
  *     float product's own rounding. A non-finite float operand makes the
  *     outputs it contributes to NaN, also where IEEE arithmetic would give an
- *     infinity. Where the result is rounded to bf16 (grad_x of a bf16 layer,
- *     the orthogonalised update of bf16 matrices) float intermediates take two
- *     parts: 2^-16 of each.
+ *     infinity. In the orthogonalised update of bf16 matrices float
+ *     intermediates take two parts: 2^-16 of each.
  * Limits: n_rows < 2^31; widths (n_in, n_out, n_cols, rows, cols) in
  * [1, 65536]; a pitch below 2^31; else UNSUPPORTED (widths below 1:
  * INVALID_ARGUMENT).
@@ -68,9 +67,9 @@ ETP_API etp_status etp_linear(int64_t n_rows, int32_t n_in, int32_t n_out, int32
  *   grad_b[j]    = sum_r d[r, j]              (float [n_out])
  * (the residual's gradient is grad_y itself). z: what etp_linear stored, NULL
  * when the activation is NONE. Outputs may be NULL (not computed); x is
- * needed for grad_W only, W for grad_x only. d is a float (three bf16 parts
- * in grad_W, whose result is float) also when the features are bf16; with
- * n_in and n_out above 128 it is kept once in the workspace.
+ * needed for grad_W only, W for grad_x only. d is a float (three bf16 parts)
+ * also when the features are bf16; with n_in and n_out above 128 it is kept
+ * once in the workspace.
  * ETP_FLAG_ACCUMULATE adds into every output given. With n_rows = 0 grad_W
  * and grad_b are zeroed (or left as they are when accumulating). ws: DEVICE,
  * 16-byte aligned, at least etp_linear_vjp_workspace() bytes, contents
