@@ -170,7 +170,7 @@ struct OrthArgs {
     void *X;
     void *ws;
 };
-size_t orthogonalize_workspace_bytes(int B, int rows, int cols, bool bf16);
+size_t orthogonalize_workspace_bytes(int B, int rows, int cols);
 hipError_t launch_orthogonalize(const OrthArgs &a, hipStream_t stream);
 
 // Sums of n sets of partial column sums: a set is n0 values that add up to

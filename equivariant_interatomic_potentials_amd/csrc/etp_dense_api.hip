@@ -178,7 +178,7 @@ etp_status etp_orthogonalize_workspace(int32_t n_mats, int32_t rows, int32_t col
     if (!bytes)
         return ETP_ERR_INVALID_ARGUMENT;
     ETP_TRY(check_mats(n_mats, rows, cols, dtype));
-    *bytes = n_mats ? etp::orthogonalize_workspace_bytes(n_mats, rows, cols, dtype == ETP_BF16) : 0;
+    *bytes = n_mats ? etp::orthogonalize_workspace_bytes(n_mats, rows, cols) : 0;
     return ETP_OK;
 }
 
@@ -196,7 +196,7 @@ etp_status etp_orthogonalize(int32_t n_mats, int32_t rows, int32_t cols, int32_t
     ETP_TRY(check_rows(G, cols, cols, e, false));
     ETP_TRY(check_rows(X, cols, cols, e, false));
     const bool bf = dtype == ETP_BF16;
-    ETP_TRY(check_ws(ws, ws_bytes, etp::orthogonalize_workspace_bytes(n_mats, rows, cols, bf)));
+    ETP_TRY(check_ws(ws, ws_bytes, etp::orthogonalize_workspace_bytes(n_mats, rows, cols)));
     etp::OrthArgs a{n_mats, rows, cols, bf, G, steps, {3.4445f, -4.7750f, 2.0315f}, eps, X, ws};
     if (coef)
         for (int i = 0; i < 3; ++i)

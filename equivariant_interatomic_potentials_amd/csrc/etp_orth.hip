@@ -2,14 +2,12 @@
 // X <- a X + (b A + c A^2) X, A = X X^T, on X / (|X|_F + eps). Everywhere X is
 // n x m with n <= m (a tall matrix is read and written transposed).
 //
-// All products run on the matrix cores on rounded bf16 parts
-// (etp_dense_mma.hpp): three for float matrices, whose small singular values
-// the steps amplify by up to a^5, so that every product has to be of float
-// quality; two (2^-17, three instructions) for bf16 ones, whose result is
-// rounded to 2^-9. (One half float of 11 bits would do for large matrices of
-// many directions, but loses 0.4% on a single one, where its roundings do not
-// average out.) A and P = b A + c A^2 are symmetric: only tiles on one side of
-// the diagonal are formed.
+// All products run on the matrix cores on three rounded bf16 parts
+// (etp_dense_mma.hpp): the steps amplify small singular values by up to a^5, so
+// that every product has to be of float quality, also for bf16 matrices (with
+// two parts one strong direction over a floor of 10^-3 comes out wrong by 10^-3
+// before the result is rounded, with three by 2 10^-5). A and P = b A + c A^2
+// are symmetric: only tiles on one side of the diagonal are formed.
 //
 //  * n <= 128: orth_strip_kernel, a workgroup per 16 W <= 128 columns. The
 //    strip of X stays in registers for all steps (a wave holds 16 columns, all
@@ -23,16 +21,15 @@
 //    for itself, updates its columns and leaves its part of the next A.
 //  * larger: three products a step over the parts in global memory, 64 x 64
 //    tiles (orth_product_kernel). 15 launches that wait for each other, each of
-//    8 to 12 us, of which a unit's loads at 64 bytes a cycle are half (two of
-//    512 x 1024 bf16: 155 us).
+//    11 to 18 us, of which a unit's loads at 64 bytes a cycle are half (two of
+//    512 x 1024: 220 us).
 #include <type_traits>
 
 #include "etp_dense_mma.hpp"
 
 namespace etp {
 
-template <typename T>
-constexpr int kOrthParts = sizeof(T) == 4 ? 3 : 2;
+constexpr int kOrthParts = 3;
 
 // ------------------------------------------------------------------- norms
 
@@ -129,7 +126,7 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 {
     // LDS row stride (elements): rows start 4 or more banks apart, so neither
     // 16 rows of 8 bytes nor 4 rows of 32 collide
-    constexpr int P = kOrthParts<T>, SN = 16 * NT + 24;
+    constexpr int P = kOrthParts, SN = 16 * NT + 24;
     constexpr int kPlane = 16 * W * SN;  // X^T: 16 W rows; A, P: 16 NT rows
     constexpr int NH = W / NT, OMAX = (NT / 2 + NH) / NH;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -416,18 +413,18 @@ constexpr int kOT = 64;  // tile
 // Results are alpha A B^T + beta D in 64 x 64 tiles. Both operands lie along
 // the contraction (X^T is kept beside X, and A, P are symmetric). There are a
 // few hundred tiles at most, so a tile takes a whole compute unit: its four
-// waves each form all of it over every fourth chunk of 64 (32 with three parts) of the contraction,
+// waves each form all of it over every fourth chunk of 32 of the contraction,
 // with fragments straight from memory into registers (nothing is shared
 // before the end, so nothing goes through LDS and no wave waits for another;
-// one wave to a SIMD has the registers for the next chunk's 24 or 16 KiB while
-// it works on this one), and the four are added in wave order. The tile leaves
+// one wave to a SIMD has the registers for the next chunk's 24 KiB while it
+// works on this one), and the four are added in wave order. The tile leaves
 // through LDS, so that it can be written along its rows and along its columns.
 constexpr int kOrthOut = kOT + 4;  // LDS row stride of the tile (floats)
 
 template <typename T, OrthOp Op>
 __global__ void __launch_bounds__(256, 1) orth_product_kernel(const OrthProductArgs a)
 {
-    constexpr int P = kOrthParts<T>, SO = kOrthOut, NH = P == 2 ? 2 : 1, KC = 32 * NH;
+    constexpr int P = kOrthParts, SO = kOrthOut;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     float *tile = reinterpret_cast<float *>(smem);  // [4][64][SO]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -455,21 +452,17 @@ __global__ void __launch_bounds__(256, 1) orth_product_kernel(const OrthProductA
     const bf16bits *A = a.A + b * P * pa + (r0 >> 4) * band + lane * 8;
     const bf16bits *B = a.B + b * P * pb + (c0 >> 4) * band + lane * 8;
 
-    Frag<P> fa[2][NH][4], fb[2][NH][4];  // [buffer][half][tile]
+    Frag<P> fa[2][4], fb[2][4];  // [buffer][tile]
     auto fetch = [&](int ch, int buf) __attribute__((always_inline)) {
-        if (KC * ch >= a.depth)
+        if (32 * ch >= a.depth)
             return;
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    fa[buf][h][i].p[p] =
-                        *reinterpret_cast<const bf16x8 *>(A + p * pa + i * band + (NH * ch + h) * 512);
-                    fb[buf][h][i].p[p] =
-                        *reinterpret_cast<const bf16x8 *>(B + p * pb + i * band + (NH * ch + h) * 512);
-                }
+            for (int p = 0; p < P; ++p) {
+                fa[buf][i].p[p] = *reinterpret_cast<const bf16x8 *>(A + p * pa + i * band + ch * 512);
+                fb[buf][i].p[p] = *reinterpret_cast<const bf16x8 *>(B + p * pb + i * band + ch * 512);
+            }
     };
     f32x4 acc[4][4];
 #pragma unroll
@@ -478,15 +471,13 @@ __global__ void __launch_bounds__(256, 1) orth_product_kernel(const OrthProductA
         for (int j = 0; j < 4; ++j)
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     fetch(wave, 0);
-    for (int ch = wave; KC * ch < a.depth; ch += 8) {
+    for (int ch = wave; 32 * ch < a.depth; ch += 8) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            if (KC * (ch + 4 * u) >= a.depth)
+            if (32 * (ch + 4 * u) >= a.depth)
                 break;
             fetch(ch + 4 * u + 4, u ^ 1);
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-                mma(fa[u][h], fb[u][h], acc);
+            mma(fa[u], fb[u], acc);
         }
     }
     float *mine = tile + wave * kOT * SO;
@@ -566,7 +557,7 @@ __global__ void __launch_bounds__(512) orth_split_kernel(const T *__restrict__ G
                                                          const int np, const int mp, bf16bits *__restrict__ X,
                                                          bf16bits *__restrict__ XT)
 {
-    constexpr int P = kOrthParts<T>;
+    constexpr int P = kOrthParts;
     __shared__ float tile[kOT][kOT + 1];  // as G lies: rows of X, or rows of X^T when tall
     const int b = blockIdx.y, rt = np / kOT, r0 = (blockIdx.x % rt) * kOT, c0 = (blockIdx.x / rt) * kOT;
     const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * 8;
@@ -614,7 +605,7 @@ struct OrthCut {
 
 static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-static OrthCut orth_cut(int B, int rows, int cols, bool bf16)
+static OrthCut orth_cut(int B, int rows, int cols)
 {
     OrthCut c{};
     c.tall = rows > cols;
@@ -637,22 +628,21 @@ static OrthCut orth_cut(int B, int rows, int cols, bool bf16)
     }
     c.np = (c.n + kOT - 1) / kOT * kOT;
     c.mp = (c.m + kOT - 1) / kOT * kOT;
-    const size_t parts = bf16 ? kOrthParts<bf16bits> : kOrthParts<float>;
-    c.x = up256(b * parts * c.np * c.mp * sizeof(bf16bits));
-    c.a = up256(b * parts * c.np * c.np * sizeof(bf16bits));
+    c.x = up256(b * kOrthParts * c.np * c.mp * sizeof(bf16bits));
+    c.a = up256(b * kOrthParts * c.np * c.np * sizeof(bf16bits));
     return c;
 }
 
-size_t orthogonalize_workspace_bytes(int B, int rows, int cols, bool bf16)
+size_t orthogonalize_workspace_bytes(int B, int rows, int cols)
 {
-    const OrthCut c = orth_cut(B, rows, cols, bf16);
+    const OrthCut c = orth_cut(B, rows, cols);
     return c.norm + 2 * c.xs + 2 * c.as + 4 * c.x + 2 * c.a;
 }
 
 template <typename T, int NT, int W>
 static hipError_t launch_strips(const StripArgs &s, hipStream_t stream)
 {
-    constexpr size_t lds = sizeof(bf16bits) * kOrthParts<T> * 16 * W * (16 * NT + 24);
+    constexpr size_t lds = sizeof(bf16bits) * kOrthParts * 16 * W * (16 * NT + 24);
     if (lds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&orth_strip_kernel<T, NT, W>),
                                                         hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -696,7 +686,7 @@ static hipError_t launch_orth_product(const OrthProductArgs &a, hipStream_t stre
 template <typename T>
 static hipError_t orthogonalize(const OrthArgs &o, hipStream_t stream)
 {
-    const OrthCut c = orth_cut(o.B, o.rows, o.cols, o.bf16);
+    const OrthCut c = orth_cut(o.B, o.rows, o.cols);
     unsigned char *ws = static_cast<unsigned char *>(o.ws);
     double *norm = reinterpret_cast<double *>(ws);
     ws += c.norm;

@@ -27,8 +27,7 @@
  *     are added in float: relative error per product below 2^-22, as a
  *     float product's own rounding. A non-finite float operand makes the
  *     outputs it contributes to NaN, also where IEEE arithmetic would give an
- *     infinity. In the orthogonalised update of bf16 matrices float
- *     intermediates take two parts: 2^-16 of each.
+ *     infinity.
  * Limits: n_rows < 2^31; widths (n_in, n_out, n_cols, rows, cols) in
  * [1, 65536]; a pitch below 2^31; else UNSUPPORTED (widths below 1:
  * INVALID_ARGUMENT).

@@ -44,3 +44,22 @@ def test_input_gradient_of_a_bf16_layer(M, N, K):
     for t in (gx, alone):
         err = (ref.f64(t) - want).abs()
         assert (err <= lim).all(), (int((err > lim).sum()), float((err / lim).max()))
+
+
+@pytest.mark.parametrize("r,c", [(128, 128), (60, 500), (200, 300), (300, 200)])
+def test_orthogonalised_bf16_is_rounded_once(r, c):
+    """bf16 matrices of one strong direction, whose steps amplify what is lost on the way by up to a^5 = 485. With float
+    quality in between (a unit of 2^-24 of |X| amplified: sigma) an entry ends on another bf16 value than the float64
+    result's only where that lies within a few sigma of a tie: at most 2 sigma / ulp of the entries of one size."""
+    import torch
+    from test_gpu_dense_orth import run
+    say("orth bf16", r, c)
+    g = torch.Generator().manual_seed(r + c)
+    G = (torch.randn(r, 1, generator=g) @ torch.randn(1, c, generator=g) + 1e-3 * torch.randn(r, c, generator=g)).bfloat16()
+    want = ref.orthogonalize(G)
+    X = ref.f64(run(G.cuda()))
+    sigma = 485 * 2.0 ** -24 * float(want.square().mean().sqrt())
+    ulp = torch.exp2(torch.floor(torch.log2(want.abs().clamp_min(1e-30))) - 7)
+    limit = float((2 * sigma / ulp).clamp_max(1.0).sum())
+    off = int((X != want.bfloat16().double()).sum())
+    assert off <= limit, (off, limit, want.numel())
