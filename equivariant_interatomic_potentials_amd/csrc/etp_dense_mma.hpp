@@ -4,11 +4,11 @@
 // q = lane / 16) holds entries k = 8 q .. 8 q + 7 of row c of the first and of
 // column c of the second operand, and rows 4 q .. 4 q + 3 of column c of the
 // float result. A float operand is cut exactly into three bf16 parts
-// (v = p0 + p1 + p2, 8 significant bits each, by truncation, so that no part
-// overflows), and the six products of parts i, j with i + j <= 2 are added in
-// float: the dropped ones are below 2^-22 of |v w|, about a float product's
-// own rounding, at six bf16 instructions of 16 cycles for 8192 products where
-// the fp32 instruction takes 256 cycles.
+// (v = p0 + p1 + p2, rounded to nearest, so |p1| <= 2^-8 |v| and |p2| <=
+// 2^-17 |v|), and the six products of parts i, j with i + j <= 2 are added in
+// float: the dropped ones are at most 2^-24 of |v w| and of either sign, a float
+// product's own rounding, at six bf16 instructions of 16 cycles for 8192
+// products where the fp32 instruction takes 256 cycles.
 #pragma once
 #include "etp_dense.hpp"
 
@@ -30,31 +30,55 @@ struct Frag {
     bf16x8 p[P];
 };
 
-__device__ __forceinline__ uint32_t high_halves(float hi, float lo)
+// How a part is taken from a float. Round: to the nearest bf16, which leaves a
+// remainder of either sign and half the size, so that the dropped products are
+// small and have no bias. Chop: the upper half of the bits, for products against
+// an operand of one part, of which none is dropped; fewer instructions (VJP
+// 441172 x 64 x 64 bf16: 51 us, 53 rounded; grad_x 32768 x 512 x 512: 90 and 93).
+enum class Cut { Round, Chop };
+template <typename T>
+constexpr Cut kCut = kParts<T> == 1 ? Cut::Chop : Cut::Round;  // against a stored T
+
+// The next part of a and b, and what remains of them. The first rounded part of
+// values above the largest bf16 (3.39e38) is that one, not infinity. (A NaN's
+// first part may be a number; its second is a NaN.)
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+template <Cut C, bool First>
+__device__ __forceinline__ uint32_t take_pair(float &a, float &b)
 {
-    return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+    uint32_t u;
+    if constexpr (C == Cut::Chop) {
+        u = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+    } else {
+        constexpr float kMost = 0x1.fep127f;
+        u = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(First ? __builtin_amdgcn_fmed3f(a, -kMost, kMost) : a),
+                                                static_cast<__bf16>(First ? __builtin_amdgcn_fmed3f(b, -kMost, kMost) : b)});
+    }
+    a -= __uint_as_float(u << 16);
+    b -= __uint_as_float(u & 0xFFFF0000u);
+    return u;
 }
 
-__device__ __forceinline__ float below_high(float v) { return v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
+// N floats as pairs of P bf16 parts; three hold them exactly.
+template <int P, Cut C, int N>
+__device__ __forceinline__ void take_parts(const float (&v)[N], uint32_t (&u)[P][N / 2])
+{
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        float a = v[2 * i], b = v[2 * i + 1];
+        u[0][i] = take_pair<C, true>(a, b);
+#pragma unroll
+        for (int p = 1; p < P; ++p)
+            u[p][i] = take_pair<C, false>(a, b);
+    }
+}
 
-// Eight floats as P bf16 parts each; P = 3 is exact, P = 2 leaves 2^-16 |v|.
-template <int P>
+template <int P, Cut C = Cut::Round>
 __device__ __forceinline__ Frag<P> split8(const float (&v)[8])
 {
     Frag<P> f;
     uint32_t u[P][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a = v[2 * i], b = v[2 * i + 1];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            u[p][i] = high_halves(b, a);
-            if (p + 1 < P) {
-                a = below_high(a);
-                b = below_high(b);
-            }
-        }
-    }
+    take_parts<P, C>(v, u);
 #pragma unroll
     for (int p = 0; p < P; ++p)
         f.p[p] = __builtin_bit_cast(bf16x8, u32x4{u[p][0], u[p][1], u[p][2], u[p][3]});
@@ -68,40 +92,6 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// split8 with rounded instead of truncated parts (nearest even): the dropped
-// products are smaller and of either sign, at the same cost, but values above
-// the largest bf16 (3.39e38) would become infinite.
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t rounded_pair(float a, float b)
-{
-    return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
-}
-__device__ __forceinline__ uint32_t take_pair(float &a, float &b)
-{
-    const uint32_t u = rounded_pair(a, b);
-    a -= __uint_as_float(u << 16);
-    b -= __uint_as_float(u & 0xFFFF0000u);
-    return u;
-}
-template <int P>
-__device__ __forceinline__ Frag<P> split8_rounded(const float (&v)[8])
-{
-    Frag<P> f;
-    float w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i] = v[i];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-        u32x4 u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = take_pair(w[2 * i], w[2 * i + 1]);
-        f.p[p] = __builtin_bit_cast(bf16x8, u);
-    }
-    return f;
 }
 
 // Eight consecutive stored values, the ones from `valid` on zero (not read).
@@ -156,10 +146,10 @@ struct Raw8<float> {
         for (int i = 0; i < 8; ++i)
             o[i] = v[i];
     }
-    template <int P>
+    template <int P, Cut C = Cut::Round>
     __device__ __forceinline__ Frag<P> frag() const
     {
-        return split8<P>(v);
+        return split8<P, C>(v);
     }
 };
 template <>
@@ -266,28 +256,19 @@ struct RawVec<bf16bits> {
     }
 };
 
-// N floats (four or eight) as P truncated parts at consecutive places of P
-// planes `plane` elements apart.
-template <int P, int N>
+// N floats (four or eight) as P parts at consecutive places of P planes `plane`
+// elements apart.
+template <int P, Cut C = Cut::Round, int N>
 __device__ __forceinline__ void put_parts(bf16bits *at, int plane, const float (&v)[N])
 {
-    float w[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        w[i] = v[i];
+    uint32_t u[P][N / 2];
+    take_parts<P, C>(v, u);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        uint32_t u[N / 2];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            u[i] = high_halves(w[2 * i + 1], w[2 * i]);
-            w[2 * i] = below_high(w[2 * i]);
-            w[2 * i + 1] = below_high(w[2 * i + 1]);
-        }
         if constexpr (N == 8)
-            *reinterpret_cast<u32x4 *>(at + p * plane) = u32x4{u[0], u[1], u[2], u[3]};
+            *reinterpret_cast<u32x4 *>(at + p * plane) = u32x4{u[p][0], u[p][1], u[p][2], u[p][3]};
         else
-            *reinterpret_cast<uint2 *>(at + p * plane) = uint2{u[0], u[1]};
+            *reinterpret_cast<uint2 *>(at + p * plane) = uint2{u[p][0], u[p][1]};
     }
 }
 

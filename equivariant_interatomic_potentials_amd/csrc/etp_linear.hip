@@ -87,7 +87,7 @@ struct RowChunk<T, Dense::Gx> {
             for (int i = 0; i < 8; ++i)
                 d[i] *= act_slope(a.act, zv[i]);
         }
-        return split8<kRowParts<T, Dense::Gx>>(d);
+        return split8<kRowParts<T, Dense::Gx>, kCut<T>>(d);
     }
 };
 
@@ -100,7 +100,7 @@ struct RowChunk<T, Dense::GxD> {
     }
     __device__ __forceinline__ Frag<kRowParts<T, Dense::GxD>> frag(const ProductArgs &) const
     {
-        return d.template frag<kRowParts<T, Dense::GxD>>();
+        return d.template frag<kRowParts<T, Dense::GxD>, kCut<T>>();
     }
 };
 
@@ -412,7 +412,7 @@ struct RowPiece {
                 if (D == Dense::Gx && a.act != kActNone)
                     f[i] *= act_slope(a.act, z.get(i));
             }
-            put_parts<kRowParts<T, D>>(at, plane, f);
+            put_parts<kRowParts<T, D>, kCut<T>>(at, plane, f);
         }
     }
 };
@@ -829,7 +829,7 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
                 d[i] = live ? d[i] : 0.f;
                 gb[i] += d[i];
             }
-            put_parts<3>(dl + row * SD + dcol, kRows * SD, d);
+            put_parts<3, kCut<T>>(dl + row * SD + dcol, kRows * SD, d);
         }
         if (want_gw) {
 #pragma unroll

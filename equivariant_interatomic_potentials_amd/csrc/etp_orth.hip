@@ -2,7 +2,7 @@
 // X <- a X + (b A + c A^2) X, A = X X^T, on X / (|X|_F + eps). Everywhere X is
 // n x m with n <= m (a tall matrix is read and written transposed).
 //
-// All products run on the matrix cores on three rounded bf16 parts
+// All products run on the matrix cores on three bf16 parts
 // (etp_dense_mma.hpp): the steps amplify small singular values by up to a^5, so
 // that every product has to be of float quality, also for bf16 matrices (with
 // two parts one strong direction over a floor of 10^-3 comes out wrong by 10^-3
@@ -15,7 +15,7 @@
 //    LDS holds the parts of X^T, then of A, then of P in the same space. With
 //    one strip (m <= 128) all steps are one launch: a matrix has one compute
 //    unit, whose matrix instructions are busy 42% of the time and wait for LDS
-//    otherwise (34 of 128 x 128 float: 73 us, five steps; spread over more
+//    otherwise (34 of 128 x 128: 76 us, five steps; spread over more
 //    units with a launch a step: 87). Wider matrices take one
 //    launch per step: each strip adds the strips' partial A in order, forms P
 //    for itself, updates its columns and leaves its part of the next A.
@@ -92,18 +92,10 @@ struct StripArgs {
     float *a_out;
 };
 
-// Four floats as P parts at consecutive places of P planes.
 template <int P>
 __device__ __forceinline__ void put4(bf16bits *at, int plane, f32x4 v)
 {
-    float w[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-        uint2 u;
-        u.x = take_pair(w[0], w[1]);
-        u.y = take_pair(w[2], w[3]);
-        *reinterpret_cast<uint2 *>(at + p * plane) = u;
-    }
+    put_parts<P>(at, plane, {v[0], v[1], v[2], v[3]});
 }
 
 // One tile (four of the eight slots) of a fragment of rows 16 r .. + 15 of a
@@ -290,7 +282,7 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] = x[2 * ch + (i >> 2)][i & 3];
-            fx[ch][0] = split8_rounded<P>(v);
+            fx[ch][0] = split8<P>(v);
         }
         constexpr int R = NT < 4 ? NT : 4;  // row tiles at a time
 #pragma unroll
@@ -495,7 +487,7 @@ __global__ void __launch_bounds__(256, 1) orth_product_kernel(const OrthProductA
     // out [rows][cols], and out_t [cols][rows] (for a symmetric result the
     // same matrix)
     auto put = [&](bf16bits *o, int row, int col, int R, int C, const float (&v)[8]) {
-        const Frag<P> f = split8_rounded<P>(v);
+        const Frag<P> f = split8<P>(v);
 #pragma unroll
         for (int p = 0; p < P; ++p)
             *reinterpret_cast<bf16x8 *>(o + (static_cast<int64_t>(b) * P + p) * R * C + part_place(row, col, C)) = f.p[p];
@@ -572,7 +564,7 @@ __global__ void __launch_bounds__(512) orth_split_kernel(const T *__restrict__ G
         tile[row][col + i] = v[i];
     }
     auto put = [&](bf16bits *o, int R, int C, int o0, int o1) {
-        const Frag<P> f = split8_rounded<P>(v);
+        const Frag<P> f = split8<P>(v);
 #pragma unroll
         for (int p = 0; p < P; ++p)
             *reinterpret_cast<bf16x8 *>(o + (static_cast<int64_t>(b) * P + p) * R * C + part_place(o0 + row, o1 + col, C)) =

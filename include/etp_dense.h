@@ -24,10 +24,10 @@
  *     rows run faster).
  *   - products are formed on the matrix cores. Float operands are split
  *     exactly into three bf16 parts each and the six leading cross products
- *     are added in float: relative error per product below 2^-22, as a
- *     float product's own rounding. A non-finite float operand makes the
- *     outputs it contributes to NaN, also where IEEE arithmetic would give an
- *     infinity.
+ *     are added in float: what is dropped is at most 2^-24 of the product
+ *     and of either sign, as a float product's own rounding. A non-finite
+ *     float operand makes the outputs it contributes to NaN, also where IEEE
+ *     arithmetic would give an infinity.
  * Limits: n_rows < 2^31; widths (n_in, n_out, n_cols, rows, cols) in
  * [1, 65536]; a pitch below 2^31; else UNSUPPORTED (widths below 1:
  * INVALID_ARGUMENT).

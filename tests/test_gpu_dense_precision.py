@@ -63,3 +63,116 @@ def test_orthogonalised_bf16_is_rounded_once(r, c):
     limit = float((2 * sigma / ulp).clamp_max(1.0).sum())
     off = int((X != want.bfloat16().double()).sum())
     assert off <= limit, (off, limit, want.numel())
+
+
+# One non-zero term in every sum: an output is a product of two floats of which
+# six partial products are added. The dropped ones are at most 2^-24 of it (a
+# part is below 2^-8 and the next below 2^-17 of the value, in two pairs), the
+# last addition rounds by 2^-23 at most (half of that to nearest), and the
+# earlier ones by 2^-8 of that: together below 1.6 * 2^-23. Two parts, or three
+# truncated ones, miss it at the mantissas tried here.
+ONE_PRODUCT = 1.6 * 2.0 ** -23
+
+
+def mantissas(n, seed):
+    """Floats of either sign and exponents of -12 .. 12; half of them with bits in the places that a part's rounding or
+    truncation costs most, the others random."""
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    u = lambda k: 2.0 ** -k
+    hard = torch.tensor([1 + u(7) - u(23), 1 + u(8) - u(23), 1 + u(8) + u(23), 1 + u(7) - u(15) - u(23), 1 + u(8) - u(16) - u(23),
+                         1 + u(8) + u(17) - u(23), 1 + u(9) + u(16), 1 + u(15) - u(23), 1 + u(16) + u(23), 2 - u(23)])
+    pick = hard[torch.randint(len(hard), (n,), generator=g)]
+    rand = 1 + torch.randint(1 << 23, (n,), generator=g).float() * u(23)
+    v = torch.where(torch.rand(n, generator=g) < 0.5, pick, rand)
+    sign = 1 - 2 * torch.randint(2, (n,), generator=g).float()
+    return v * sign * torch.exp2(torch.randint(-12, 13, (n,), generator=g).float())
+
+
+def one_per_row(M, K, seed):
+    """[M, K] with one non-zero in every row, in column r % K."""
+    import torch
+    x = torch.zeros(M, K)
+    r = torch.arange(M)
+    x[r, r % K] = mantissas(M, seed)
+    return x
+
+
+def check_products(got, want, what):
+    err = (ref.f64(got) - want).abs()
+    bad = err > ONE_PRODUCT * want.abs()
+    assert not bad.any(), (what, int(bad.sum()), float((err / want.abs().clamp_min(1e-300)).max()) * 2.0 ** 23)
+
+
+# resident matrix of 32, 64, 96 and 128 inputs; few rows of a long contraction; tiles of 32, 64 and 128 columns by 64
+# and 128 rows
+FORWARD = [(300, 32, 64), (300, 50, 130), (2000, 96, 128), (260, 128, 257), (130, 300, 65), (16500, 140, 30),
+           (66000, 130, 20), (16500, 140, 64), (66000, 130, 64), (16500, 140, 130), (40000, 130, 200)]
+
+
+@pytest.mark.parametrize("M,K,N", FORWARD)
+def test_single_products_forward(M, K, N):
+    from equivariant_interatomic_potentials_amd import dense
+    import torch
+    say("single products", M, K, N)
+    x, W = one_per_row(M, K, M), mantissas(K * N, N).view(K, N)
+    y = out(M, N, torch.float32)
+    dense.etp_linear(x.cuda(), W.cuda(), y)
+    r = torch.arange(M) % K
+    check_products(y, x.double().sum(1, keepdim=True) * W.double()[r], "y")
+
+
+# every block of the panel kernel, gradients in blocks, and input gradients as products of their own
+VJP = [(300, 32, 32), (300, 20, 64), (300, 32, 128), (300, 64, 30), (400, 64, 64), (300, 64, 128), (300, 128, 32),
+       (300, 128, 64), (2000, 128, 128), (500, 200, 100), (500, 100, 200), (700, 260, 300), (17000, 200, 140),
+       (17000, 140, 200)]
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("M,K,N", VJP)
+def test_single_products_vjp(M, K, N, act):
+    """With SiLU, z = 0: its slope is one half exactly, and d = gy / 2."""
+    import torch
+    from equivariant_interatomic_potentials_amd import dense
+    say("single products, VJP", M, K, N, act)
+    half = 0.5 if act == "silu" else 1.0
+    gy, W = one_per_row(M, N, M), mantissas(K * N, N).view(K, N)
+    x = torch.zeros(M, K)
+    top = min(M, N)
+    x[:top] = mantissas(top * K, 1).view(top, K)  # row j meets the one entry of gy in column j
+    z = torch.zeros(M, N, device="cuda") if act == "silu" else None
+    gx, gW, gx_alone = out(M, K, torch.float32), torch.full((K, N), float("nan"), device="cuda"), out(M, K, torch.float32)
+    dense.etp_linear_vjp(x.cuda(), W.cuda(), gy.cuda(), z, ref.ACTS[act], gx, gW, None, workspace(M, K, N, torch.float32))
+    dense.etp_linear_vjp(None, W.cuda(), gy.cuda(), z, ref.ACTS[act], gx_alone)
+    d = half * gy.double().sum(1)
+    want = d[:, None] * W.double().T[torch.arange(M) % N]
+    check_products(gx, want, "grad_x")
+    check_products(gx_alone, want, "grad_x alone")
+    gw = torch.zeros(K, N, dtype=torch.float64)
+    gw[:, :top] = x[:top].double().T * d[:top]
+    check_products(gW, gw, "grad_W")
+
+
+@pytest.mark.parametrize("K,N", [(64, 64), (200, 40), (200, 300)])
+def test_largest_floats(K, N):
+    """Floats above the largest bf16 (3.39e38) are split like the others."""
+    import torch
+    from equivariant_interatomic_potentials_amd import dense
+    say("largest floats", K, N)
+    M, top = 600, torch.finfo(torch.float32).max
+    x = torch.zeros(M, K)
+    r = torch.arange(M)
+    x[r, r % K] = torch.where(r % 2 == 0, top, -3.396e38)
+    W = (mantissas(K * N, 5).abs().view(K, N) * 2.0 ** -14)
+    y = out(M, N, torch.float32)
+    dense.etp_linear(x.cuda(), W.cuda(), y)
+    check_products(y, x.double().sum(1, keepdim=True) * W.double()[r % K], "y")
+    gW = torch.full((K, N), float("nan"), device="cuda")
+    gy = one_per_row(M, N, 2) * 2.0 ** -14
+    lead = min(M, N)
+    x = torch.zeros(M, K)
+    x[:lead] = top
+    dense.etp_linear_vjp(x.cuda(), W.cuda(), gy.cuda(), None, 0, None, gW, None, workspace(M, K, N, torch.float32))
+    gw = torch.zeros(K, N, dtype=torch.float64)
+    gw[:, :lead] = x[:lead].double().T * gy[:lead].double().sum(1)
+    check_products(gW, gw, "grad_W")
