@@ -4,14 +4,16 @@
 // Both are one pass over the data, bound by HBM. LPR lanes (a power of two up
 // to the wave) own a row and hold it in registers, 16 bytes a load, so that
 // mean, variance (from the differences) and the result come from one read;
-// sums over the row are exchanges between the LPR lanes. A lane keeps the same
-// columns for every row it meets, so gamma and beta are read once and the
-// VJP's column sums grow in registers; waves walk the rows with the grid's
-// stride and load the next row while they work on the present one. Rows of
-// more than 2048 columns take a workgroup each and read the row again (from
-// cache) for every sum.
+// sums over the row are exchanges between the LPR lanes. The mean is taken
+// twice, of the row and of the differences from that, so that rows with a
+// common offset (constant ones among them) keep the digits of their spread
+// (32768 x 512 bf16 12.4 -> 12.7 us). A lane keeps the same columns for every
+// row it meets, so gamma and beta are read once and the VJP's column sums grow
+// in registers; waves walk the rows with the grid's stride and load the next
+// row while they work on the present one. Rows of more than 2048 columns take a
+// workgroup each and read the row again (from cache) for every sum.
 //
-// Measured: forward 32768 x 512 bf16 12.4 us (5.4 TB/s, part of it from
+// Measured: forward 32768 x 512 bf16 12.7 us (5.3 TB/s, part of it from
 // cache); VJP 441172 x 64 float 66 us (5.2 TB/s), 5184 x 777 bf16 16 us (1.5
 // TB/s: two launches, and rows of 1554 bytes on any alignment), 50000 x 2000
 // float 240 us (5.0 TB/s).
@@ -49,7 +51,7 @@ __device__ __forceinline__ float group_sum(float v)
 }
 
 // s / c from inv = 1 / c with one correction, so that a quotient that is a
-// float comes out exactly (the mean of a constant row is its value).
+// float comes out exactly.
 __device__ __forceinline__ float quotient(float s, float c, float inv)
 {
     const float m = s * inv;
@@ -144,13 +146,25 @@ __global__ void __launch_bounds__(256) layer_norm_kernel(const NormArgs a)
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 s += cs.own(n, i) ? x[n][i] : 0.f;
-        const float mean = quotient(group_sum<LPR>(s), static_cast<float>(a.C), inv);
-        float v = 0.f;
+        float mean = quotient(group_sum<LPR>(s), static_cast<float>(a.C), inv);
+        // the row's sum has rounded at the size of its values: the differences,
+        // at the size of their spread, give what the mean is off by
+        s = 0.f;
 #pragma unroll
         for (int n = 0; n < NI; ++n)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 x[n][i] = cs.own(n, i) ? x[n][i] - mean : 0.f;
+                s += x[n][i];
+            }
+        const float off = group_sum<LPR>(s) * inv;
+        mean += off;
+        float v = 0.f;
+#pragma unroll
+        for (int n = 0; n < NI; ++n)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[n][i] = cs.own(n, i) ? x[n][i] - off : 0.f;
                 v = __builtin_fmaf(x[n][i], x[n][i], v);
             }
         const float rstd = 1.f / sqrtf(__builtin_fmaf(group_sum<LPR>(v), inv, a.eps));
@@ -300,10 +314,20 @@ __global__ void __launch_bounds__(64 * kVjpWaves) layer_norm_vjp_kernel(const No
 
 // --------------------------------------------------------------- long rows
 
-// sum over the workgroup's 256 threads, in every thread
-__device__ __forceinline__ float block_sum(float v, float *lds)
+__device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
+__device__ __forceinline__ double wave_sum(double v)
 {
-    v = group_sum<64>(v);
+#pragma unroll
+    for (int m = 32; m; m >>= 1)
+        v += __shfl_xor(v, m);
+    return v;
+}
+
+// sum over the workgroup's 256 threads, in every thread
+template <typename S>
+__device__ __forceinline__ S block_sum(S v, S *lds)
+{
+    v = wave_sum(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0)
         lds[threadIdx.x >> 6] = v;
@@ -315,22 +339,26 @@ template <typename T>
 __global__ void __launch_bounds__(256) layer_norm_long_kernel(const NormArgs a)
 {
     __shared__ float lds[4];
+    __shared__ double wide[4];
     const float inv = 1.f / static_cast<float>(a.C);
     for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
         const T *x = static_cast<const T *>(a.x) + r * a.ldx;
-        float s = 0.f;
+        // the mean as a float and what that is off by, from a double sum (another
+        // pass over the differences, as for short rows, took 15 to 30% longer)
+        double s = 0.0;
         for (int c = threadIdx.x; c < a.C; c += 256)
             s += to_f32(x[c]);
-        const float mean = quotient(block_sum(s, lds), static_cast<float>(a.C), inv);
+        s = block_sum(s, wide) / a.C;
+        const float mean = static_cast<float>(s), off = static_cast<float>(s - mean);
         float q = 0.f;
         for (int c = threadIdx.x; c < a.C; c += 256) {
-            const float d = to_f32(x[c]) - mean;
+            const float d = to_f32(x[c]) - mean - off;
             q = __builtin_fmaf(d, d, q);
         }
         const float rstd = 1.f / sqrtf(__builtin_fmaf(block_sum(q, lds), inv, a.eps));
         T *y = static_cast<T *>(a.y) + r * a.ldy;
         for (int c = threadIdx.x; c < a.C; c += 256)
-            y[c] = from_f32<T>(__builtin_fmaf((to_f32(x[c]) - mean) * rstd, a.gamma ? a.gamma[c] : 1.f,
+            y[c] = from_f32<T>(__builtin_fmaf((to_f32(x[c]) - mean - off) * rstd, a.gamma ? a.gamma[c] : 1.f,
                                               a.beta ? a.beta[c] : 0.f));
         if (threadIdx.x == 0) {
             if (a.mean)

@@ -90,8 +90,9 @@ ETP_API etp_status etp_linear_vjp_workspace(int64_t n_rows, int32_t n_in, int32_
  *   y[r, c] = (x[r, c] - mean) rstd gamma[c] + beta[c]
  * x, y: dtype, pitches ldx, ldy; gamma, beta: float [n_cols] or NULL (1 and
  * 0); mean, rstd: float [n_rows], written when not NULL (the VJP needs both).
- * eps: finite, > 0. The variance is summed from the differences in float.
- * Errors: as etp_linear. */
+ * eps: finite, > 0. y is formed from differences that a common offset of the
+ * row costs no digits; the variance is summed from them in float. Errors: as
+ * etp_linear. */
 ETP_API etp_status etp_layer_norm(int64_t n_rows, int32_t n_cols, int32_t dtype, const void *x, int64_t ldx,
                                   const float *gamma, const float *beta, float eps, void *y, int64_t ldy,
                                   float *mean, float *rstd, void *stream);
