@@ -68,14 +68,29 @@ __global__ void __launch_bounds__(256) orth_norm_kernel(const T *__restrict__ G,
         part[blockIdx.y * kNormParts + blockIdx.x] = lds[0];
 }
 
-// 1 / (|G_b|_F + eps) from the partial sums, in every lane
-__device__ __forceinline__ float orth_scale(const double *part, int b, float eps)
+// 1 / (|G|_F + eps) as m 2^e: it can pass a float on either side (a zero matrix
+// and a small eps; entries near the largest float, whose norm is larger than
+// any), an entry times it cannot.
+struct OrthScale {
+    float m;
+    int e;
+    __device__ __forceinline__ OrthScale(double squares, float eps)
+    {
+        const double v = 1.0 / (sqrt(squares) + eps);
+        m = static_cast<float>(__builtin_amdgcn_frexp_mant(v));
+        e = __builtin_amdgcn_frexp_exp(v);
+    }
+    __device__ __forceinline__ float operator()(float v) const { return m * __builtin_amdgcn_ldexpf(v, e); }
+};
+
+// the sum of squares of matrix b from its partial sums, in every lane
+__device__ __forceinline__ double orth_squares(const double *part, int b)
 {
     double s = part[b * kNormParts + (threadIdx.x & 63)];
 #pragma unroll
     for (int m = 32; m; m >>= 1)
         s += __shfl_xor(s, m);
-    return static_cast<float>(1.0 / (sqrt(s) + eps));
+    return s;
 }
 
 // ------------------------------------------------------------------ strips
@@ -157,12 +172,11 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
                                                 : static_cast<int64_t>(row) * m + col])
                               : 0.f;
             }
-        float scale;
+        double t = 0.0;
         if (s.norm) {
-            scale = orth_scale(s.norm, b, s.o.eps);
+            t = orth_squares(s.norm, b);
         } else {
             // all of the matrix by every workgroup of it
-            double t = 0.0;
             for (int64_t i = threadIdx.x; i < nm; i += 64 * W) {
                 const double v = to_f32(G[i]);
                 t = __builtin_fma(v, v, t);
@@ -177,11 +191,13 @@ __global__ void __launch_bounds__(64 * W) orth_strip_kernel(const StripArgs s)
 #pragma unroll
             for (int w = 1; w < W; ++w)
                 t += red[w];
-            scale = static_cast<float>(1.0 / (sqrt(t) + s.o.eps));
         }
+        const OrthScale scale(t, s.o.eps);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-            x[i] *= scale;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x[i][r] = scale(x[i][r]);
     } else {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -557,10 +573,10 @@ __global__ void __launch_bounds__(512) orth_split_kernel(const T *__restrict__ G
     const int valid = gr0 + row < gr ? gc - gc0 - col : 0;
     float v[8];
     load8(G + (static_cast<int64_t>(b) * gr + (valid > 0 ? gr0 + row : 0)) * gc + (valid > 0 ? gc0 + col : 0), valid, v);
-    const float scale = orth_scale(norm, b, eps);
+    const OrthScale scale(orth_squares(norm, b), eps);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        v[i] *= scale;
+        v[i] = scale(v[i]);
         tile[row][col + i] = v[i];
     }
     auto put = [&](bf16bits *o, int R, int C, int o0, int o1) {

@@ -176,3 +176,24 @@ def test_largest_floats(K, N):
     gw = torch.zeros(K, N, dtype=torch.float64)
     gw[:, :lead] = x[:lead].double().T * gy[:lead].double().sum(1)
     check_products(gW, gw, "grad_W")
+
+
+@pytest.mark.parametrize("r,c", [(1, 1), (24, 40), (128, 128), (60, 500), (200, 300), (300, 200)])
+def test_scale_beyond_a_float(r, c):
+    """1 / (|G|_F + eps) is not always a float: a zero matrix with an eps below 2^-128 stays zero, and entries near the
+    largest float (a scale below the smallest normal float) give what the same matrix gives at any other scale."""
+    import torch
+    from test_gpu_dense_orth import make, run
+    say("orth scale", r, c)
+    for dtype in TYPES:
+        zero = torch.zeros(2, r, c, dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda")
+        assert (run(zero, eps=1e-40) == 0).all()
+        G = make(1, r, c, dtype, 4, scale=0.25)
+        big = G * 2.0 ** 125  # exact
+        assert torch.isfinite(big).all()
+        assert torch.equal(run(big, eps=1e-30), run(G, eps=1e-40))
+        small = G * 2.0 ** -120
+        X = run(small, eps=1e-45)
+        if dtype == "f32":  # (entries below the smallest normal float keep fewer bits)
+            want = ref.orthogonalize(small, eps=1e-45)
+            assert float((ref.f64(X) - want).norm()) <= 1.2e-4 * float(want.norm())
