@@ -695,6 +695,7 @@ struct PanelArgs {
     int nsplit;       // workgroups along the panels
     int nkb;          // blocks of 32 KC along K (1 with gx)
     int blocks;       // of gW
+    int64_t set;      // floats of a partial set: gW, then gb, of those that are wanted
 };
 
 // With eight waves and one workgroup a compute unit, two panels' parts lie in
@@ -943,7 +944,7 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
     if (S.bufs == 2)
         lds_barrier();  // the sums below reuse the space
 
-    float *part = static_cast<float *>(a.ws) + static_cast<int64_t>(s) * (static_cast<int64_t>(K) + 1) * N;
+    float *part = static_cast<float *>(a.ws) + s * p.set;
     if (want_gw) {
 #pragma unroll
         for (int i = 0; i < KT; ++i)
@@ -971,7 +972,7 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
             for (int r = 0; r < RD; ++r)
                 v += sums[r * 32 * NC + j];
             if (j0 + j < N)
-                part[static_cast<int64_t>(K) * N + j0 + j] = v;
+                part[p.set - N + j0 + j] = v;
         }
     }
 }
@@ -1068,7 +1069,9 @@ hipError_t launch_linear(const LinearArgs &a, hipStream_t stream)
 // How a VJP call is cut: all in one panel kernel where K and N are at most
 // 128, else gx as a product and gW in blocks of up to 128 x 128, with d made
 // once before both where K and N are above 128 (where only one is, forming d
-// again costs less than keeping it).
+// again costs less than keeping it). gb without gW needs the blocks along N
+// only, as if there were one input (gx is a product of its own then, unless
+// the one panel kernel forms it on the way).
 struct VjpCut {
     bool fused, keep_d;  // one kernel for all; d made once
     int kc, nc;          // chunks of 32 of a block: 1, 2 or 4
@@ -1113,7 +1116,8 @@ size_t linear_vjp_workspace_bytes(int64_t M, int K, int N, bool bf16)
     if (M == 0)
         return 0;
     const VjpCut v = vjp_cut(M, K, N, bf16);
-    return v.d_bytes + v.part_bytes;
+    const size_t all = v.d_bytes + v.part_bytes, bias = vjp_cut(M, 1, N, bf16).part_bytes;
+    return all > bias ? all : bias;
 }
 
 template <typename T, int KC, int NC, bool FromD>
@@ -1151,11 +1155,10 @@ static hipError_t panel_by_shape(const PanelArgs &p, const VjpCut &v, hipStream_
 }
 
 template <typename T>
-static hipError_t linear_vjp(const LinearVjpArgs &a, hipStream_t stream)
+static hipError_t linear_vjp(const LinearVjpArgs &a, const VjpCut &v, int64_t set, hipStream_t stream)
 {
-    const bool sums = a.gW || a.gb;
-    const VjpCut v = vjp_cut(a.M, a.K, a.N, a.bf16);
-    PanelArgs p{a, nullptr, v.npanel, v.nsplit, v.nkb, v.nkb * v.nnb};
+    const bool sums = set > 0;
+    PanelArgs p{a, nullptr, v.npanel, v.nsplit, v.nkb, v.nkb * v.nnb, set};
     hipError_t e = hipSuccess;
     if (!v.fused || !sums) {
         // without the sums there is no workspace either: d as the product goes
@@ -1180,16 +1183,20 @@ static hipError_t linear_vjp(const LinearVjpArgs &a, hipStream_t stream)
 
 hipError_t launch_linear_vjp(const LinearVjpArgs &a, hipStream_t stream)
 {
-    const bool sums = a.gW || a.gb;
+    const int64_t n0 = a.gW ? static_cast<int64_t>(a.K) * a.N : 0, n1 = a.gb ? a.N : 0;
     hipError_t e = hipSuccess;
     int nsplit = 0;
     if (a.M > 0) {
-        nsplit = vjp_cut(a.M, a.K, a.N, a.bf16).nsplit;
-        e = a.bf16 ? linear_vjp<bf16bits>(a, stream) : linear_vjp<float>(a, stream);
+        VjpCut v = vjp_cut(a.M, a.K, a.N, a.bf16);
+        if (!a.gW && !(v.fused && a.gx)) {
+            v = vjp_cut(a.M, 1, a.N, a.bf16);
+            v.fused = false;
+        }
+        nsplit = v.nsplit;
+        e = a.bf16 ? linear_vjp<bf16bits>(a, v, n0 + n1, stream) : linear_vjp<float>(a, v, n0 + n1, stream);
     }
-    if (e == hipSuccess && sums)
-        e = launch_sum_parts(static_cast<int64_t>(a.K) * a.N, a.gW, a.N, a.gb, nsplit,
-                             static_cast<const float *>(a.ws), a.accumulate, stream);
+    if (e == hipSuccess && n0 + n1 > 0)
+        e = launch_sum_parts(n0, a.gW, n1, a.gb, nsplit, static_cast<const float *>(a.ws), a.accumulate, stream);
     return e;
 }
 

@@ -71,7 +71,8 @@ ETP_API etp_status etp_linear(int64_t n_rows, int32_t n_in, int32_t n_out, int32
  * once in the workspace.
  * ETP_FLAG_ACCUMULATE adds into every output given. With n_rows = 0 grad_W
  * and grad_b are zeroed (or left as they are when accumulating). ws: DEVICE,
- * 16-byte aligned, at least etp_linear_vjp_workspace() bytes, contents
+ * 16-byte aligned, at least etp_linear_vjp_workspace() bytes (which count d
+ * also for an activation of NONE, where it is grad_y itself), contents
  * undefined afterwards; needed for grad_W and grad_b. Errors: as etp_linear,
  * plus WORKSPACE (ws missing, misaligned or too small), INVALID_ARGUMENT
  * (other flags). */

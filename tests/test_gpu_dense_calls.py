@@ -1,0 +1,47 @@
+"""Calls of the dense operators' VJPs for a part of their outputs, and the
+binding's checks of matrix shapes."""
+import pytest
+
+import dense_reference as ref
+from test_gpu_dense_linear import TYPES, make, out, say, workspace
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,N", [(1, 5, 3), (300, 64, 64), (2000, 300, 90), (1500, 257, 400), (5000, 1000, 130)])
+def test_bias_gradient_alone(M, K, N, dtype):
+    """grad_b without grad_W is a sum over d only: its partial sums are all that the call keeps in the workspace."""
+    import torch
+    from equivariant_interatomic_potentials_amd import dense
+    say("grad_b alone", M, K, N, dtype)
+    p = make(M, K, N, dtype, M + N)
+    ws = workspace(M, K, N, p["dt"])
+    gb = torch.full((N,), float("nan"), device="cuda")
+    dense.etp_linear_vjp(None, p["W"], p["gy"], p["z"], 1, None, None, gb, ws)
+    ref.close(gb, ref.linear_vjp(p["x"], p["W"], p["gy"], p["z"], "silu")[2])
+    assert (ws[4 * N * ((M + 31) // 32):] == 0xFF).all()  # a set for each 32 rows at most
+    was = gb.clone()
+    dense.etp_linear_vjp(None, p["W"], p["gy"], p["z"], 1, None, None, gb, ws, dense.ETP_FLAG_ACCUMULATE)
+    assert torch.equal(gb, was + was)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,N", [(0, 6, 7), (300, 64, 64), (700, 200, 50), (700, 50, 200), (900, 260, 300)])
+def test_every_subset_of_the_gradients(M, K, N, dtype):
+    """The workspace holds what any subset needs, and what is not asked for is not written."""
+    import torch
+    from equivariant_interatomic_potentials_amd import dense
+    say("linear_vjp subsets", M, K, N, dtype)
+    p = make(M, K, N, dtype, M + K)
+    want = ref.linear_vjp(p["x"], p["W"], p["gy"], p["z"], "gelu")
+    for which in range(1, 8):
+        new = [out(M, K, p["dt"]), torch.full((K, N), float("nan"), device="cuda"), torch.full((N,), float("nan"), device="cuda")]
+        o = [t if which >> i & 1 else None for i, t in enumerate(new)]
+        size = dense.etp_linear_vjp_workspace(M, K, N, p["dt"])
+        ws = torch.full((size + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        dense.etp_linear_vjp(p["x"], p["W"], p["gy"], p["z"], 2, *o, ws[:size] if size else None)
+        assert (ws[size:] == 0xFF).all()
+        for t, r in zip(o, want):
+            if t is not None:
+                ref.close(t, r)
