@@ -426,7 +426,7 @@ struct NormShape {
     int lpr, ni;
 };
 
-static NormShape norm_shape(int C, int V, bool vjp)
+static constexpr NormShape norm_shape(int C, int V, bool vjp)
 {
     const int vecs = (C + V - 1) / V, most = vjp && V == 8 ? 2 : 4;
     int lpr = 1;
@@ -442,16 +442,26 @@ static NormShape norm_shape(int C, int V, bool vjp)
     return {lpr, ni};
 }
 
-// Calls f(LPR, NI, RAG) for the shape s of rows of C columns in vectors of V.
-template <int V, typename F>
-static hipError_t by_shape(NormShape s, int C, F &&f)
+// Calls f(LPR, NI, RAG) for rows of C columns in vectors of V; only shapes that
+// some row has are compiled.
+template <int V, bool Vjp, int LPR, int NI>
+constexpr bool norm_shape_taken()
 {
-#define ETP_NORM_CASE(L, N)                                                                       \
-    if (s.lpr == L && s.ni == N)                                                                  \
-        return C == L * N * V ? f(std::integral_constant<int, L>{}, std::integral_constant<int, N>{}, \
-                                  std::false_type{})                                              \
-                              : f(std::integral_constant<int, L>{}, std::integral_constant<int, N>{}, \
-                                  std::true_type{});
+    constexpr NormShape s = norm_shape(LPR * NI * V, V, Vjp);  // (a shape's longest row is a full one)
+    return LPR * NI * V <= kLongRow && s.lpr == LPR && s.ni == NI;
+}
+
+template <int V, bool Vjp, typename F>
+static hipError_t by_shape(int C, F &&f)
+{
+    const NormShape s = norm_shape(C, V, Vjp);
+#define ETP_NORM_CASE(L, N)                                                                                   \
+    if constexpr (norm_shape_taken<V, Vjp, L, N>())                                                           \
+        if (s.lpr == L && s.ni == N)                                                                          \
+            return C == L * N * V ? f(std::integral_constant<int, L>{}, std::integral_constant<int, N>{},     \
+                                      std::false_type{})                                                      \
+                                  : f(std::integral_constant<int, L>{}, std::integral_constant<int, N>{},     \
+                                      std::true_type{});
     ETP_NORM_CASE(1, 1)
     ETP_NORM_CASE(2, 1)
     ETP_NORM_CASE(4, 1)
@@ -463,9 +473,7 @@ static hipError_t by_shape(NormShape s, int C, F &&f)
     ETP_NORM_CASE(32, 4)
     ETP_NORM_CASE(64, 2)
     ETP_NORM_CASE(64, 4)
-    if constexpr (V == 4) {
-        ETP_NORM_CASE(64, 8)
-    }
+    ETP_NORM_CASE(64, 8)
 #undef ETP_NORM_CASE
     return hipErrorInvalidValue;
 }
@@ -489,7 +497,7 @@ static hipError_t norm_forward(const NormArgs &a, hipStream_t stream)
         hipLaunchKernelGGL(layer_norm_long_kernel<T>, dim3(norm_grid(a.M, 1, 2048)), dim3(256), 0, stream, a);
         return hipGetLastError();
     }
-    return by_shape<kVec<T>>(norm_shape(a.C, kVec<T>, false), a.C, [&](auto l, auto n, auto rag) {
+    return by_shape<kVec<T>, false>(a.C, [&](auto l, auto n, auto rag) {
         hipLaunchKernelGGL((layer_norm_kernel<T, l(), n(), rag()>), dim3(norm_grid(a.M, 64 / l(), 1024)), dim3(256), 0,
                            stream, a);
         return hipGetLastError();
@@ -537,7 +545,7 @@ static hipError_t norm_vjp(const NormVjpArgs &a, int S, hipStream_t stream)
                                dim3(256), 0, stream, a, S);
         return hipGetLastError();
     }
-    return by_shape<kVec<T>>(norm_shape(a.C, kVec<T>, true), a.C, [&](auto l, auto n, auto rag) {
+    return by_shape<kVec<T>, true>(a.C, [&](auto l, auto n, auto rag) {
         hipLaunchKernelGGL((layer_norm_vjp_kernel<T, l(), n(), rag()>), dim3(static_cast<unsigned>(S)),
                            dim3(64 * kVjpWaves), 0, stream, a);
         return hipGetLastError();

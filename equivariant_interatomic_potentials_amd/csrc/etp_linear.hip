@@ -608,6 +608,32 @@ static hipError_t launch_resident(const ProductArgs &a, dim3 grid, dim3 block, s
     return hipGetLastError();
 }
 
+// As many workgroups as LDS and 16 waves a compute unit let run at once, in
+// eighths of the chip. (Kernels of more than 128 registers, most input gradients
+// and the float forwards of more than 64 inputs, run 8 or 12 of those waves and
+// leave the last workgroups to a second round.)
+template <typename T, Dense D>
+static hipError_t launch_resident_product(const ProductArgs &a, hipStream_t stream)
+{
+    const int kc = (a.KD + 31) / 32;
+    const int nb = a.ND <= 64 ? 64 : 128, nsplit = (a.ND + nb - 1) / nb;
+    const size_t lds = sizeof(bf16bits) * kc * MatrixLds<T, D>::chunk(nb) + nb * sizeof(float);
+    const int waves = lds <= 40 * 1024 ? 4 : 8;
+    const int per_cu = static_cast<int>(160 * 1024 / lds) < 16 / waves ? static_cast<int>(160 * 1024 / lds)
+                                                                        : 16 / waves;
+    int64_t streams = ((a.M + 15) / 16 + waves - 1) / waves;
+    const int64_t most = kComputeUnits * per_cu / nsplit / 8 * 8;
+    streams = (streams + 7) / 8 * 8;
+    streams = streams < most ? streams : most < 8 ? 8 : most;
+    const dim3 grid(static_cast<unsigned>(streams * nsplit)), block(64 * waves);
+    switch (kc) {
+    case 1: return launch_resident<T, D, 1>(a, grid, block, lds, nb, nsplit, stream);
+    case 2: return launch_resident<T, D, 2>(a, grid, block, lds, nb, nsplit, stream);
+    case 3: return launch_resident<T, D, 3>(a, grid, block, lds, nb, nsplit, stream);
+    default: return launch_resident<T, D, 4>(a, grid, block, lds, nb, nsplit, stream);
+    }
+}
+
 template <typename T, Dense D, int RT, int kCols>
 static hipError_t launch_stream(const ProductArgs &a, int ncol, hipStream_t stream)
 {
@@ -624,25 +650,10 @@ template <typename T, Dense D>
 static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
 {
     const int64_t ntile = (a.M + 15) / 16;
-    if (a.KD <= 128) {
-        const int kc = (a.KD + 31) / 32;
-        const int nb = a.ND <= 64 ? 64 : 128, nsplit = (a.ND + nb - 1) / nb;
-        const size_t lds = sizeof(bf16bits) * kc * MatrixLds<T, D>::chunk(nb) + nb * sizeof(float);
-        const int waves = lds <= 40 * 1024 ? 4 : 8;
-        const int per_cu = static_cast<int>(160 * 1024 / lds) < 16 / waves ? static_cast<int>(160 * 1024 / lds)
-                                                                            : 16 / waves;
-        int64_t streams = (ntile + waves - 1) / waves;
-        // no more than run at once, in eighths of the chip
-        const int64_t most = kComputeUnits * per_cu / nsplit / 8 * 8;
-        streams = (streams + 7) / 8 * 8;
-        streams = streams < most ? streams : most < 8 ? 8 : most;
-        const dim3 grid(static_cast<unsigned>(streams * nsplit)), block(64 * waves);
-        switch (kc) {
-        case 1: return launch_resident<T, D, 1>(a, grid, block, lds, nb, nsplit, stream);
-        case 2: return launch_resident<T, D, 2>(a, grid, block, lds, nb, nsplit, stream);
-        case 3: return launch_resident<T, D, 3>(a, grid, block, lds, nb, nsplit, stream);
-        default: return launch_resident<T, D, 4>(a, grid, block, lds, nb, nsplit, stream);
-        }
+    // (d is kept for layers of more than 128 inputs and outputs only)
+    if constexpr (D != Dense::GxD) {
+        if (a.KD <= 128)
+            return launch_resident_product<T, D>(a, stream);
     }
     const int ncol = (a.ND + 127) / 128;
     const int64_t wide = (a.M + 127) / 128 * ncol, half = (a.M + 63) / 64 * ncol;
@@ -652,7 +663,7 @@ static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
                            a, nc);
         return hipGetLastError();
     }
-    if constexpr (D != Dense::GxD) {  // (d is kept for wide layers only)
+    if constexpr (D != Dense::GxD) {
         if (a.ND <= 32)
             return wide < 2 * kComputeUnits ? launch_stream<T, D, 2, 32>(a, 1, stream)
                                             : launch_stream<T, D, 4, 32>(a, 1, stream);
