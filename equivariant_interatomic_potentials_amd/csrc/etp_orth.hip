@@ -730,6 +730,8 @@ static hipError_t orthogonalize(const OrthArgs &o, hipStream_t stream)
     const unsigned rt = c.np / kOT, ct = c.mp / kOT;
     hipLaunchKernelGGL(orth_split_kernel<T>, dim3(rt * ct, o.B), dim3(512), 0, stream, G, norm, o.eps, c.n, c.m,
                        c.tall, c.np, c.mp, X[0], XT[0]);
+    if ((e = hipGetLastError()) != hipSuccess)
+        return e;
     const int sym = static_cast<int>(rt * (rt + 1) / 2), all = static_cast<int>(rt * ct);
     for (int k = 0; k < o.steps; ++k) {
         const int i = k & 1;

@@ -40,3 +40,19 @@ def test_every_layer_norm_kernel_is_taken_by_some_row():
         for typ, vec in (("float", 4), ("unsigned short", 8)):
             want = {shape(-(-c // vec), 2 if vjp and vec == 8 else 4) for c in range(1, 2049)}
             assert {k[1:3] for k in kernels(name) if k[0] == typ} == want
+
+
+def test_every_launch_is_checked():
+    """A refused launch is reported by the call that made it, not by a later one: hipGetLastError follows each launch
+    before the next launch or runtime call."""
+    files = [f for f in sorted(os.listdir(CSRC)) if f in ("etp_linear.hip", "etp_layer_norm.hip", "etp_orth.hip")]
+    assert len(files) == 3
+    for f in files:
+        text = open(os.path.join(CSRC, f)).read()
+        launches = [m.end() for m in re.finditer(r"hipLaunchKernelGGL\(", text)]
+        assert launches
+        for i, at in enumerate(launches):
+            rest = text[at:]
+            check, other = rest.find("hipGetLastError"), re.search(r"hipFuncSetAttribute|\n}\n", rest)
+            stop = other.start() if other else len(rest)
+            assert 0 <= check < stop, (f, text[:at].count("\n") + 1)
