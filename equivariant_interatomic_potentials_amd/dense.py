@@ -137,9 +137,14 @@ def etp_linear_vjp_workspace(n_rows: int, n_in: int, n_out: int, dtype=torch.flo
 def etp_linear_vjp(x, W, grad_y, z=None, activation: int = ETP_ACT_NONE, grad_x=None, grad_W=None, grad_b=None,
                    ws=None, flags: int = 0, stream=None):
     """VJP of etp_linear: grad_x [M, K], grad_W float [K, N], grad_b float [N] (each optional; x may be None without
-    grad_W); ws: etp_linear_vjp_workspace(M, K, N, dtype) bytes."""
+    grad_W, W without grad_x); ws: etp_linear_vjp_workspace(M, K, N, dtype) bytes."""
     M, N = _matrix(grad_y, "grad_y")
-    K, dt = W.shape[0], grad_y.dtype
+    dt = grad_y.dtype
+    if W is not None:
+        K = W.shape[0]
+    else:
+        given = x if x is not None else grad_x
+        K = 1 if given is None else _matrix(given, "x" if x is not None else "grad_x")[1]  # (grad_b has no K)
     code = _code(dt)
     xp, ldx = _rows(x, "x", dt, M, K, True)
     zp, ldz = _rows(z, "z", dt, M, N, True)
@@ -147,7 +152,7 @@ def etp_linear_vjp(x, W, grad_y, z=None, activation: int = ETP_ACT_NONE, grad_x=
     op, ldo = _rows(grad_x, "grad_x", dt, M, K, True)
     wp, wb = _workspace(ws)
     f32 = torch.float32
-    _check(lib.etp_linear_vjp(M, K, N, code, xp, ldx, _dense(W, "W", dt, K * N), zp, ldz, activation, gp, ldg, op, ldo,
+    _check(lib.etp_linear_vjp(M, K, N, code, xp, ldx, _dense(W, "W", dt, K * N, True), zp, ldz, activation, gp, ldg, op, ldo,
                               _dense(grad_W, "grad_W", f32, K * N, True),
                               _dense(grad_b, "grad_b", f32, N, True), flags, wp, wb, _stream(stream, grad_y)),
            "etp_linear_vjp")

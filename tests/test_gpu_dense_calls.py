@@ -45,3 +45,23 @@ def test_every_subset_of_the_gradients(M, K, N, dtype):
         for t, r in zip(o, want):
             if t is not None:
                 ref.close(t, r)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_weight_is_needed_for_the_input_gradient_only(dtype):
+    import torch
+    from equivariant_interatomic_potentials_amd import dense
+    M, K, N = 120, 40, 72
+    say("linear_vjp without W", dtype)
+    p = make(M, K, N, dtype, 3)
+    want = ref.linear_vjp(p["x"], p["W"], p["gy"], p["z"], "silu")
+    gW, gb = torch.full((K, N), float("nan"), device="cuda"), torch.full((N,), float("nan"), device="cuda")
+    ws = workspace(M, K, N, p["dt"])
+    dense.etp_linear_vjp(p["x"], None, p["gy"], p["z"], 1, None, gW, gb, ws)
+    ref.close(gW, want[1])
+    ref.close(gb, want[2])
+    gb.fill_(float("nan"))
+    dense.etp_linear_vjp(None, None, p["gy"], p["z"], 1, None, None, gb, ws)
+    ref.close(gb, want[2])
+    with pytest.raises(dense.EtpError):
+        dense.etp_linear_vjp(None, None, p["gy"], p["z"], 1, out(M, K, p["dt"]))
