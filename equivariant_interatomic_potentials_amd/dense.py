@@ -99,6 +99,13 @@ def _dense(t, name, dtype, numel, optional=False):
     return t.data_ptr()
 
 
+def _dense_matrix(t, name, dtype, rows, cols, n_mats=1, optional=False):
+    """_dense of [rows][cols] matrices back to back: flat, or with that shape in the last two dimensions."""
+    if t is not None and t.dim() > 1 and t.shape[-2:] != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}][{cols}], got {list(t.shape)}")
+    return _dense(t, name, dtype, n_mats * rows * cols, optional)
+
+
 def _workspace(ws):
     return (None, 0) if ws is None else (_dense(ws, "ws", ws.dtype, ws.numel()), ws.numel() * ws.element_size())
 
@@ -125,7 +132,7 @@ def etp_linear(x, W, y, bias=None, activation: int = ETP_ACT_NONE, residual=None
     rp, ldr = _rows(residual, "residual", dt, M, N, True)
     yp, ldy = _rows(y, "y", dt, M, N)
     zp, ldz = _rows(z, "z", dt, M, N, True)
-    _check(lib.etp_linear(M, K, N, code, xp, ldx, _dense(W, "W", dt, K * N),
+    _check(lib.etp_linear(M, K, N, code, xp, ldx, _dense_matrix(W, "W", dt, K, N),
                           _dense(bias, "bias", torch.float32, N, True), activation, rp, ldr, yp, ldy, zp, ldz,
                           _stream(stream, x)), "etp_linear")
 
@@ -146,14 +153,15 @@ def etp_linear_vjp(x, W, grad_y, z=None, activation: int = ETP_ACT_NONE, grad_x=
         given = x if x is not None else grad_x
         K = 1 if given is None else _matrix(given, "x" if x is not None else "grad_x")[1]  # (grad_b has no K)
     code = _code(dt)
+    Wp = _dense_matrix(W, "W", dt, K, N, optional=True)
     xp, ldx = _rows(x, "x", dt, M, K, True)
     zp, ldz = _rows(z, "z", dt, M, N, True)
     gp, ldg = _rows(grad_y, "grad_y", dt, M, N)
     op, ldo = _rows(grad_x, "grad_x", dt, M, K, True)
     wp, wb = _workspace(ws)
     f32 = torch.float32
-    _check(lib.etp_linear_vjp(M, K, N, code, xp, ldx, _dense(W, "W", dt, K * N, True), zp, ldz, activation, gp, ldg, op, ldo,
-                              _dense(grad_W, "grad_W", f32, K * N, True),
+    _check(lib.etp_linear_vjp(M, K, N, code, xp, ldx, Wp, zp, ldz, activation, gp, ldg, op, ldo,
+                              _dense_matrix(grad_W, "grad_W", f32, K, N, optional=True),
                               _dense(grad_b, "grad_b", f32, N, True), flags, wp, wb, _stream(stream, grad_y)),
            "etp_linear_vjp")
 
@@ -206,7 +214,8 @@ def etp_orthogonalize(G, X, steps: int = 5, coef=None, eps: float = 1e-7, ws=Non
     n = G.shape[0] if G.dim() == 3 else 1
     dt = G.dtype
     code = _code(dt)
+    r, k = G.shape[-2:]
     wp, wb = _workspace(ws)
     c = None if coef is None else (ctypes.c_float * 3)(*coef)
-    _check(lib.etp_orthogonalize(n, G.shape[-2], G.shape[-1], code, _dense(G, "G", dt, G.numel()), steps, c, eps,
-                                 _dense(X, "X", dt, G.numel()), wp, wb, _stream(stream, G)), "etp_orthogonalize")
+    _check(lib.etp_orthogonalize(n, r, k, code, _dense(G, "G", dt, G.numel()), steps, c, eps,
+                                 _dense_matrix(X, "X", dt, r, k, n), wp, wb, _stream(stream, G)), "etp_orthogonalize")

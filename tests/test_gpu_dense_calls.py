@@ -65,3 +65,24 @@ def test_weight_is_needed_for_the_input_gradient_only(dtype):
     ref.close(gb, want[2])
     with pytest.raises(dense.EtpError):
         dense.etp_linear_vjp(None, None, p["gy"], p["z"], 1, out(M, K, p["dt"]))
+
+
+def test_transposed_matrices_are_refused():
+    """A buffer of the right size in the other orientation would be filled with a scrambled matrix."""
+    import torch
+    from equivariant_interatomic_potentials_amd import dense
+    M, K, N = 30, 40, 72
+    say("linear_vjp shapes")
+    p = make(M, K, N, "f32", 3)
+    ws = workspace(M, K, N, p["dt"])
+    with pytest.raises(ValueError, match="grad_W"):
+        dense.etp_linear_vjp(p["x"], p["W"], p["gy"], p["z"], 1, None, torch.empty(N, K, device="cuda"), None, ws)
+    with pytest.raises(ValueError, match="W"):
+        dense.etp_linear_vjp(p["x"], p["W"].view(2 * K, N // 2), p["gy"], p["z"], 1, out(M, K, p["dt"]))
+    flat = torch.full((K * N,), float("nan"), device="cuda")  # a slice of one long buffer of gradients
+    dense.etp_linear_vjp(p["x"], p["W"], p["gy"], p["z"], 1, None, flat, None, ws)
+    ref.close(flat.view(K, N), ref.linear_vjp(p["x"], p["W"], p["gy"], p["z"], "silu")[1])
+    G = torch.randn(24, 36, device="cuda")
+    ws = torch.empty(dense.etp_orthogonalize_workspace(1, 24, 36), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="X"):
+        dense.etp_orthogonalize(G, torch.empty(36, 24, device="cuda"), ws=ws)
