@@ -86,3 +86,22 @@ def test_transposed_matrices_are_refused():
     ws = torch.empty(dense.etp_orthogonalize_workspace(1, 24, 36), dtype=torch.uint8, device="cuda")
     with pytest.raises(ValueError, match="X"):
         dense.etp_orthogonalize(G, torch.empty(36, 24, device="cuda"), ws=ws)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("M,K,N", [(70001, 64, 64), (70001, 64, 128), (40000, 128, 30), (50000, 20, 96), (33000, 300, 128)])
+def test_input_gradient_alone_on_many_rows(M, K, N, act, dtype):
+    """What forces need, at row counts that fill the chip several times over, with and without accumulation."""
+    import torch
+    from equivariant_interatomic_potentials_amd import dense
+    say("grad_x alone", M, K, N, act, dtype)
+    p = make(M, K, N, dtype, M + K)
+    want = ref.linear_vjp(p["x"], p["W"], p["gy"], p["z"], act)[0]
+    z = None if act == "none" else p["z"]
+    gx = out(M, K, p["dt"])
+    dense.etp_linear_vjp(None, p["W"], p["gy"], z, ref.ACTS[act], gx)
+    ref.close(gx, want)
+    base = p["x"].clone()
+    dense.etp_linear_vjp(None, p["W"], p["gy"], z, ref.ACTS[act], base, flags=dense.ETP_FLAG_ACCUMULATE)
+    ref.close(base, ref.f64(p["x"]) + want)

@@ -197,3 +197,34 @@ def test_scale_beyond_a_float(r, c):
         if dtype == "f32":  # (entries below the smallest normal float keep fewer bits)
             want = ref.orthogonalize(small, eps=1e-45)
             assert float((ref.f64(X) - want).norm()) <= 1.2e-4 * float(want.norm())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_between_the_tails(act):
+    """Value and slope on a dense grid of [-6, 6]. SiLU: the logistic function errs by three units (2^-22 of it), its
+    complement as a float by as much absolutely, times 1 + |z| in the slope. GELU: the fitted polynomial is within 8e-6
+    of the tail (3.7e-9 of Phi), the float evaluation of its eight terms, the exponential of z^2 / 2 and 1 - tail add
+    2^-21 of Phi and 2^-19 of the tail; the slope adds z times the density, an exponential of its own."""
+    import torch
+    from equivariant_interatomic_potentials_amd import dense
+    say("activations", act)
+    n = 120001
+    z = torch.linspace(-6, 6, n)[:, None]
+    one = torch.ones(1, 1, device="cuda")
+    y, gx = out(n, 1, torch.float32), out(n, 1, torch.float32)
+    dense.etp_linear(z.cuda(), one, y, None, ref.ACTS[act])
+    dense.etp_linear_vjp(None, one, torch.ones_like(y), z.cuda(), ref.ACTS[act], gx)
+    zd = z.double()
+    if act == "silu":
+        s = torch.sigmoid(zd)
+        lim_y, lim_s = 2.0 ** -21 * s * zd.abs(), 2.0 ** -21 * s * (1 + zd.abs())
+    else:
+        tail = 0.5 * torch.erfc(zd.abs() / 2 ** 0.5)
+        phi = torch.where(zd > 0, 1 - tail, tail)
+        lim_phi = 2.0 ** -21 * phi + (8e-6 + 2.0 ** -19) * tail
+        density = torch.exp(-zd * zd / 2) / (2 * torch.pi) ** 0.5
+        lim_y = lim_phi * zd.abs() + 2.0 ** -23 * phi * zd.abs()
+        lim_s = lim_phi + (2.0 ** -22 * (1 + zd * zd)) * zd.abs() * density + 2.0 ** -23
+    for t, r, lim in ((y, ref.act(act, zd), lim_y), (gx, ref.act_slope(act, zd), lim_s)):
+        err = (ref.f64(t) - r).abs()
+        assert (err <= lim + 1e-30).all(), (float((err / (lim + 1e-30)).max()), float(zd[(err / (lim + 1e-30)).argmax()]))
