@@ -59,7 +59,8 @@ __device__ __forceinline__ uint32_t take_pair(float &a, float &b)
     return u;
 }
 
-// N floats as pairs of P bf16 parts; three hold them exactly.
+// N floats as pairs of P bf16 parts; three hold them exactly (below 2^-110, where
+// the last is subnormal, to 2^-134).
 template <int P, Cut C, int N>
 __device__ __forceinline__ void take_parts(const float (&v)[N], uint32_t (&u)[P][N / 2])
 {

@@ -25,9 +25,11 @@
  *   - products are formed on the matrix cores. Float operands are split
  *     exactly into three bf16 parts each and the six leading cross products
  *     are added in float: what is dropped is at most 2^-24 of the product
- *     and of either sign, as a float product's own rounding. A non-finite
- *     float operand makes the outputs it contributes to NaN, also where IEEE
- *     arithmetic would give an infinity.
+ *     and of either sign, as a float product's own rounding. (Operands below
+ *     2^-110 are held to 2^-134 absolutely.) A non-finite float operand makes
+ *     the outputs it contributes to NaN, also where IEEE arithmetic would
+ *     give an infinity; so does a bf16 one in the VJP, whose other factor d is
+ *     a float.
  * Limits: n_rows < 2^31; widths (n_in, n_out, n_cols, rows, cols) in
  * [1, 65536]; a pitch below 2^31; else UNSUPPORTED (widths below 1:
  * INVALID_ARGUMENT).

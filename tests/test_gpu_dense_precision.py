@@ -228,3 +228,25 @@ def test_activations_between_the_tails(act):
     for t, r, lim in ((y, ref.act(act, zd), lim_y), (gx, ref.act_slope(act, zd), lim_s)):
         err = (ref.f64(t) - r).abs()
         assert (err <= lim + 1e-30).all(), (float((err / (lim + 1e-30)).max()), float(zd[(err / (lim + 1e-30)).argmax()]))
+
+
+@pytest.mark.parametrize("K,N", [(64, 64), (200, 40), (200, 300)])
+def test_smallest_floats(K, N):
+    """Below 2^-110 the last part is a subnormal bf16 of the unit 2^-133: half of that times the other factor."""
+    import torch
+    from equivariant_interatomic_potentials_amd import dense
+    say("smallest floats", K, N)
+    M = 600
+    r = torch.arange(M)
+    v = mantissas(M, 6)
+    v = v / torch.exp2(torch.floor(torch.log2(v.abs()))) * torch.exp2(-(100 + r % 26).float())
+    W = mantissas(K * N, 5).view(K, N)
+    x, gy = torch.zeros(M, K), torch.zeros(M, N)
+    x[r, r % K], gy[r, r % N] = v, v
+    y, gx = out(M, N, torch.float32), out(M, K, torch.float32)
+    dense.etp_linear(x.cuda(), W.cuda(), y)
+    dense.etp_linear_vjp(None, W.cuda(), gy.cuda(), None, 0, gx)
+    for got, w in ((y, W.double()[r % K]), (gx, W.double().T[r % N])):
+        want = v.double()[:, None] * w
+        err = (ref.f64(got) - want).abs()
+        assert (err <= ONE_PRODUCT * want.abs() + 2.0 ** -134 * w.abs() + 2.0 ** -149).all()
