@@ -143,7 +143,7 @@ struct MatrixLds {
     // place of quarter q of column c in a tile: columns one after the other,
     // their quarters turned so that neither the stores (a column's four
     // quarters by consecutive threads) nor the reads (a quarter of 16 columns)
-    // collide: 32768 x 512 x 512 bf16, 50.1 -> 47.8 us
+    // collide: 32768 x 512 x 512 bf16 grad_x, 50.1 -> 47.8 us
     static __device__ __forceinline__ int swizzled(int c, int q) { return 4 * c + (q ^ ((c >> 2) & 3)); }
 
     // piece i of the chunk from k0: consecutive threads along W's rows
@@ -319,8 +319,9 @@ __device__ __forceinline__ void load_group_addend(const ProductArgs &a, int64_t 
 // take to come and go, so what counts is loads ahead (the next tile's are in
 // flight during this one's products) and whole 64-byte stores: 441172 x 64 x 64
 // float with residual and z 105 us, 4.3 TB/s (a large copy: 5.0); 32768 x 128
-// x 512 bf16 with z 25 us, 3.0 TB/s, of which 5 us are the launch's start and
-// the matrix's way into LDS.
+// x 512 bf16 with z 25.5 us, 3.0 TB/s, of which 5 us are the launch's start and
+// the matrix's way into LDS. grad_x alone, 441172 x 64 x 64: float 85 us, 4.0
+// TB/s, bf16 33 us.
 template <typename T, Dense D, int KC>
 __global__ void __launch_bounds__(512) product_resident_kernel(const ProductArgs a, const int nb, const int nsplit)
 {
@@ -428,8 +429,8 @@ struct RowPiece {
 // waves one below the other, where 128 would mostly multiply zeros: 441172 x
 // 256 x 8 float 176 -> 98 us, 4.9 TB/s, x 64 bf16 129 -> 78 us, 4.3 TB/s. Wide
 // ones are bound by LDS reads and matrix instructions taking turns: 32768 x
-// 512 x 512 forward float 120 us (a library's float product of that size: 115
-// at its best rate), bf16 44 us.
+// 512 x 512 forward float 113 to 130 us (a library's float product of that
+// size: 115 at its best rate), bf16 42 to 47 us.
 template <typename T, Dense D, int RT, int kCols>
 __global__ void __launch_bounds__(256, kCols == 128 ? 2 : kCols == 64 ? 3 : 4) product_stream_kernel(const ProductArgs a, const int ncol)
 {
@@ -690,15 +691,13 @@ static hipError_t launch_product(const ProductArgs &a, hipStream_t stream)
 // registers from d itself. With K and N above 128 the same kernel forms a 128
 // x 128 block of gW per workgroup (no gx) from d made once by slope_kernel.
 //
-// With narrow layers HBM bounds it (5172508 x 64 x 64 bf16: 535 us, 4.9 TB/s;
-// 131072 x 64 x 128 float: 54 us, 3.7 TB/s, where forming and writing the
-// parts, reading the fragments and the products take about a third each and
-// two workgroups a compute unit overlap them in part). In 128 x 128 blocks
-// (32768 x 512 x 512 bf16: 77 of the call's 144 us) matrix instructions are
-// busy for 49 of 155 thousand cycles, LDS for 57, the vector units for 57: one
-// workgroup a compute unit, so they hardly overlap; two would need 128
-// registers a lane and spill.
-//
+// With narrow layers HBM bounds it (5172508 x 64 x 64 bf16: 549 us, 4.8 TB/s).
+// 131072 x 64 x 128 float: 55 us, 3.6 TB/s; of 100 thousand cycles the vector
+// units (forming the parts) are busy for 49, LDS for 29, matrix instructions for
+// 25, overlapped in part by the eight waves of the one workgroup a compute unit
+// (two would fit LDS, but not the registers: 128 a lane, and spill). In 128 x
+// 128 blocks (32768 x 512 x 512 bf16: 78 of the call's 156 us) it is 69, 57 and
+// 49 of 151 thousand, again with one workgroup a compute unit; two would spill.
 struct PanelArgs {
     LinearVjpArgs v;
     const float *d;   // d [M][N], or null: from gy and z
@@ -713,8 +712,9 @@ struct PanelArgs {
 // LDS, and while one feeds the products the next is formed and written: one
 // barrier a panel, of 64 rows, or 32 where two of 64 do not fit. Otherwise one
 // panel of 64 rows, so that several workgroups share a compute unit and fill
-// each other's waits: wherever their accumulators fit the registers (200000 x
-// 128 x 64 bf16, 52 -> 46 us; 128 x 128 bf16 would spill, 78 -> 132 us).
+// each other's waits: for bf16 wherever their accumulators fit the registers
+// (200000 x 128 x 64 takes 13% longer with one workgroup of two buffers; 128 x
+// 128 would spill, 78 -> 132 us), for float up to 64 x 64.
 struct PanelShape {
     int px, waves, sx, sd, bufs, rows, lds, per_cu;  // parts of x, row strides (elements), workgroups that fit
     constexpr PanelShape(bool bf16, int kc, int nc)
@@ -741,10 +741,10 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
     // workgroup i runs on XCD i % 8: the blocks that read the same panels run
-    // on one of them, so that its L2 serves all but the first (20000 x 384 x
-    // 1024 bf16, with the splits cut to one round: 202 -> 155 us). A single
-    // block has nothing to share and walks in step (5172508 x 64 x 64 bf16:
-    // 535 us, 549 by XCD).
+    // on one of them, so that its L2 serves all but the first (with the splits
+    // cut to one round it saved a quarter of 20000 x 384 x 1024 bf16). A
+    // single block has nothing to share and walks in step (by XCD 5172508 x 64
+    // x 64 bf16 takes 2.6% longer).
     const int total = p.nsplit * p.blocks, each = (total + 7) / 8;
     const int id = p.blocks > 1 ? (blockIdx.x & 7) * each + (blockIdx.x >> 3) : blockIdx.x;
     if (id >= total)
@@ -988,10 +988,10 @@ __global__ void __launch_bounds__((64 * kPanelShape<T, KC, NC>.waves),
     }
 }
 
-// d = gy act'(z) in float, dense rows: 32768 x 512 bf16, 25 us at 5.2 TB/s.
+// d = gy act'(z) in float, dense rows: 32768 x 512 bf16, 27 us at 4.9 TB/s.
 // (Kept as three bf16 parts instead, the blocks' vector work shrinks and their
-// reads grow by half: 143 against 145 us for 32768 x 512 x 512 bf16, 256
-// against 249 for float.)
+// reads grow by half: the call of 32768 x 512 x 512 took 1% less for bf16 and 3%
+// more for float.)
 template <typename T>
 __global__ void __launch_bounds__(256) slope_kernel(const LinearVjpArgs a, float *__restrict__ d)
 {

@@ -14,14 +14,14 @@
 //    n rows, in accumulator layout, which is also the operand layout of P X);
 //    LDS holds the parts of X^T, then of A, then of P in the same space. With
 //    one strip (m <= 128) all steps are one launch: a matrix has one compute
-//    unit, whose matrix instructions are busy 42% of the time and wait for LDS
-//    otherwise (34 of 128 x 128: 76 us, five steps; spread over more
-//    units with a launch a step: 87). Wider matrices take one
-//    launch per step: each strip adds the strips' partial A in order, forms P
+//    unit, whose matrix instructions are busy 38% of the time and LDS 58%, in
+//    turns (34 of 128 x 128: 76 us, five steps; spread over more units with a
+//    launch a step it took a fifth longer). Wider matrices take one launch per
+//    step: each strip adds the strips' partial A in order, forms P
 //    for itself, updates its columns and leaves its part of the next A.
 //  * larger: three products a step over the parts in global memory, 64 x 64
 //    tiles (orth_product_kernel). 15 launches that wait for each other, each of
-//    11 to 18 us, of which a unit's loads at 64 bytes a cycle are half (two of
+//    12 to 17 us, of which a unit's loads at 64 bytes a cycle are a third (two of
 //    512 x 1024: 220 us).
 #include <type_traits>
 

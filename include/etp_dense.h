@@ -8,7 +8,10 @@
  * its VJP hands back grad_h. These calls are those hidden layers -- a linear
  * layer with bias, activation and residual, and the layer norm -- with their
  * VJPs, and the orthogonalised update of a weight matrix (of these layers, of
- * W_r, or of the channel-mixing blocks).
+ * W_r, or of the channel-mixing blocks). There is no VJP of the VJPs here: a
+ * loss on forces, which differentiates grad_x of these layers once more, needs
+ * the caller's own second pass through them (etp_edge_conv_vjp2_radial is that
+ * of the convolution).
  *
  * Conventions as in etp.h: statuses, streams, ownership, DEVICE pointers
  * owned by the caller, validation on the host before any launch, no
