@@ -174,6 +174,26 @@ struct OrthArgs {
 size_t orthogonalize_workspace_bytes(int B, int rows, int cols);
 hipError_t launch_orthogonalize(const OrthArgs &a, hipStream_t stream);
 
+// The linear layer with a matrix for each group of rows: W, bias, gW and gb are
+// those of group 0, the others follow.
+struct GroupedLinearArgs {
+    LinearArgs l;
+    int n_groups;
+    const int *group_ptr, *order;
+};
+hipError_t launch_grouped_linear(const GroupedLinearArgs &a, hipStream_t stream);
+
+struct GroupedLinearVjpArgs {
+    LinearVjpArgs v;
+    int n_groups;
+    const int *group_ptr, *order;
+};
+size_t grouped_linear_vjp_workspace_bytes(int64_t M, int G, int K, int N, bool bf16);
+hipError_t launch_grouped_linear_vjp(const GroupedLinearVjpArgs &a, hipStream_t stream);
+
+size_t group_rows_workspace_bytes(int64_t M, int G);
+hipError_t launch_group_rows(int64_t M, int G, const int *ids, int *ptr, int *order, void *ws, hipStream_t stream);
+
 // Sums of n sets of partial column sums: a set is n0 values that add up to
 // out0 and n1 more for out1 (either output may be null: not written); n = 0
 // writes zeros. Accumulating adds to what the outputs hold.

@@ -4,10 +4,12 @@
 
 #include "../../include/etp_dense.h"
 #include "etp_dense.hpp"
+#include "etp_grad_norm.hpp"
 
 namespace {
 
-constexpr int kMaxWidth = 65536;
+constexpr int kMaxWidth = 65536, kMaxGroups = 65535;
+constexpr int64_t kMaxEntries = int64_t{1} << 43;
 
 etp_status status_of(hipError_t e) { return e == hipSuccess ? ETP_OK : ETP_ERR_HIP; }
 
@@ -202,6 +204,156 @@ etp_status etp_orthogonalize(int32_t n_mats, int32_t rows, int32_t cols, int32_t
         for (int i = 0; i < 3; ++i)
             a.coef[i] = coef[i];
     return status_of(etp::launch_orthogonalize(a, static_cast<hipStream_t>(stream)));
+}
+
+static etp_status check_groups(int64_t n_rows, int32_t n_groups)
+{
+    if (n_rows < 0 || n_groups < 1)
+        return ETP_ERR_INVALID_ARGUMENT;
+    return n_rows >= (int64_t{1} << 31) || n_groups > kMaxGroups ? ETP_ERR_UNSUPPORTED : ETP_OK;
+}
+
+etp_status etp_group_rows_workspace(int64_t n_rows, int32_t n_groups, size_t *bytes)
+{
+    if (!bytes)
+        return ETP_ERR_INVALID_ARGUMENT;
+    ETP_TRY(check_groups(n_rows, n_groups));
+    *bytes = etp::group_rows_workspace_bytes(n_rows, n_groups);
+    return ETP_OK;
+}
+
+etp_status etp_group_rows(int64_t n_rows, int32_t n_groups, const int32_t *ids, int32_t *group_ptr, int32_t *order,
+                          void *ws, size_t ws_bytes, void *stream)
+{
+    ETP_TRY(check_groups(n_rows, n_groups));
+    if (!group_ptr || (n_rows > 0 && (!ids || !order)) || misaligned(ids, 4) || misaligned(group_ptr, 4) ||
+        misaligned(order, 4))
+        return ETP_ERR_INVALID_ARGUMENT;
+    ETP_TRY(check_ws(ws, ws_bytes, etp::group_rows_workspace_bytes(n_rows, n_groups)));
+    return status_of(
+        etp::launch_group_rows(n_rows, n_groups, ids, group_ptr, order, ws, static_cast<hipStream_t>(stream)));
+}
+
+etp_status etp_grouped_linear(int64_t n_rows, int32_t n_groups, const int32_t *group_ptr, const int32_t *order,
+                              int32_t n_in, int32_t n_out, int32_t dtype, const void *x, int64_t ldx, const void *W,
+                              const float *bias, int32_t activation, const void *residual, int64_t ldr, void *y,
+                              int64_t ldy, void *z, int64_t ldz, void *stream)
+{
+    ETP_TRY(check_sizes(n_rows, n_in, n_out, dtype));
+    ETP_TRY(check_groups(n_rows, n_groups));
+    if (activation < ETP_ACT_NONE || activation > ETP_ACT_GELU)
+        return ETP_ERR_INVALID_ARGUMENT;
+    if (n_rows == 0)
+        return ETP_OK;
+    const size_t e = dtype == ETP_BF16 ? 2 : 4;
+    ETP_TRY(check_rows(x, ldx, n_in, e, false));
+    ETP_TRY(check_rows(W, n_out, n_out, e, false));
+    ETP_TRY(check_rows(y, ldy, n_out, e, false));
+    ETP_TRY(check_rows(residual, ldr, n_out, e, true));
+    ETP_TRY(check_rows(z, ldz, n_out, e, true));
+    if (!group_ptr || misaligned(group_ptr, 4) || misaligned(order, 4) || misaligned(bias, 4))
+        return ETP_ERR_INVALID_ARGUMENT;
+    const etp::GroupedLinearArgs a{{n_rows, n_in, n_out, dtype == ETP_BF16, x, ldx, W, bias, activation, residual, ldr,
+                                    y, ldy, z, ldz},
+                                   n_groups, group_ptr, order};
+    return status_of(etp::launch_grouped_linear(a, static_cast<hipStream_t>(stream)));
+}
+
+etp_status etp_grouped_linear_vjp_workspace(int64_t n_rows, int32_t n_groups, int32_t n_in, int32_t n_out,
+                                            int32_t dtype, size_t *bytes)
+{
+    if (!bytes)
+        return ETP_ERR_INVALID_ARGUMENT;
+    ETP_TRY(check_sizes(n_rows, n_in, n_out, dtype));
+    ETP_TRY(check_groups(n_rows, n_groups));
+    *bytes = etp::grouped_linear_vjp_workspace_bytes(n_rows, n_groups, n_in, n_out, dtype == ETP_BF16);
+    return ETP_OK;
+}
+
+etp_status etp_grouped_linear_vjp(int64_t n_rows, int32_t n_groups, const int32_t *group_ptr, const int32_t *order,
+                                  int32_t n_in, int32_t n_out, int32_t dtype, const void *x, int64_t ldx,
+                                  const void *W, const void *z, int64_t ldz, int32_t activation, const void *grad_y,
+                                  int64_t ldgy, void *grad_x, int64_t ldgx, float *grad_W, float *grad_b,
+                                  uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    ETP_TRY(check_sizes(n_rows, n_in, n_out, dtype));
+    ETP_TRY(check_groups(n_rows, n_groups));
+    if (activation < ETP_ACT_NONE || activation > ETP_ACT_GELU)
+        return ETP_ERR_INVALID_ARGUMENT;
+    if (flags & ~static_cast<uint32_t>(ETP_FLAG_ACCUMULATE))
+        return ETP_ERR_INVALID_ARGUMENT;
+    const size_t e = dtype == ETP_BF16 ? 2 : 4;
+    if (n_rows > 0) {
+        ETP_TRY(check_rows(x, ldx, n_in, e, !grad_W));
+        ETP_TRY(check_rows(W, n_out, n_out, e, !grad_x));
+        ETP_TRY(check_rows(z, ldz, n_out, e, activation == ETP_ACT_NONE));
+        ETP_TRY(check_rows(grad_y, ldgy, n_out, e, !grad_x && !grad_W && !grad_b));
+        ETP_TRY(check_rows(grad_x, ldgx, n_in, e, true));
+    }
+    const bool any = grad_W || grad_b || (n_rows > 0 && grad_x);
+    if ((any && !group_ptr) || misaligned(group_ptr, 4) || misaligned(order, 4) || misaligned(grad_W, 4) ||
+        misaligned(grad_b, 4))
+        return ETP_ERR_INVALID_ARGUMENT;
+    if (!any)
+        return ETP_OK;
+    const bool bf = dtype == ETP_BF16;
+    if (grad_W || grad_b)
+        ETP_TRY(check_ws(ws, ws_bytes, etp::grouped_linear_vjp_workspace_bytes(n_rows, n_groups, n_in, n_out, bf)));
+    const etp::GroupedLinearVjpArgs a{{n_rows, n_in, n_out, bf, (flags & ETP_FLAG_ACCUMULATE) != 0, x, ldx, W, z, ldz,
+                                       activation, grad_y, ldgy, grad_x, ldgx, grad_W, grad_b, ws},
+                                      n_groups, group_ptr, order};
+    return status_of(etp::launch_grouped_linear_vjp(a, static_cast<hipStream_t>(stream)));
+}
+
+static etp_status check_tensors(int32_t n_tensors, const etp_tensor *grads, bool data)
+{
+    if (n_tensors < 0 || (n_tensors > 0 && !grads))
+        return ETP_ERR_INVALID_ARGUMENT;
+    etp_status st = ETP_OK;
+    for (int i = 0; i < n_tensors; ++i) {
+        const etp_tensor &t = grads[i];
+        if (t.numel < 0 || (t.dtype != ETP_F32 && t.dtype != ETP_BF16))
+            return ETP_ERR_INVALID_ARGUMENT;
+        if (data && t.numel > 0 && (!t.data || misaligned(t.data, t.dtype == ETP_BF16 ? 2 : 4)))
+            return ETP_ERR_INVALID_ARGUMENT;
+        if (t.numel >= kMaxEntries)
+            st = ETP_ERR_UNSUPPORTED;
+    }
+    return st;
+}
+
+etp_status etp_grad_norm_workspace(int32_t n_tensors, const etp_tensor *grads, size_t *bytes)
+{
+    if (!bytes)
+        return ETP_ERR_INVALID_ARGUMENT;
+    ETP_TRY(check_tensors(n_tensors, grads, false));
+    *bytes = etp::grad_norm_workspace_bytes({n_tensors, grads, nullptr});
+    return ETP_OK;
+}
+
+etp_status etp_grad_norm(int32_t n_tensors, const etp_tensor *grads, float *norm, void *ws, size_t ws_bytes,
+                         void *stream)
+{
+    ETP_TRY(check_tensors(n_tensors, grads, true));
+    if (!norm || misaligned(norm, 4))
+        return ETP_ERR_INVALID_ARGUMENT;
+    const etp::GradList list{n_tensors, grads, nullptr};
+    ETP_TRY(check_ws(ws, ws_bytes, etp::grad_norm_workspace_bytes(list)));
+    return status_of(etp::launch_grad_norm(list, norm, ws, static_cast<hipStream_t>(stream)));
+}
+
+etp_status etp_clip_grads(int32_t n_tensors, const etp_tensor *grads, float max_norm, void *const *out, float *norm,
+                          void *ws, size_t ws_bytes, void *stream)
+{
+    ETP_TRY(check_tensors(n_tensors, grads, true));
+    if (!std::isfinite(max_norm) || max_norm < 0.f || misaligned(norm, 4))
+        return ETP_ERR_INVALID_ARGUMENT;
+    for (int i = 0; out && i < n_tensors; ++i)
+        if (grads[i].numel > 0 && (!out[i] || misaligned(out[i], grads[i].dtype == ETP_BF16 ? 2 : 4)))
+            return ETP_ERR_INVALID_ARGUMENT;
+    const etp::GradList list{n_tensors, grads, out};
+    ETP_TRY(check_ws(ws, ws_bytes, etp::grad_norm_workspace_bytes(list)));
+    return status_of(etp::launch_clip_grads(list, max_norm, norm, ws, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

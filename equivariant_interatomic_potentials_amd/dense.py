@@ -1,12 +1,15 @@
 """Thin Python binding of libetp's dense operators (include/etp_dense.h), same
 names as the C ABI: the linear layer and the layer norm of the radial and node
-networks with their VJPs, and the orthogonalised update of weight matrices.
+networks with their VJPs, the linear layer with a matrix for each group of rows
+(elements, pairs of elements) and the grouping of rows by type, the norm of all
+gradients with clipping, and the orthogonalised update of weight matrices.
 
 As in ``etp``: argument marshalling only, torch's current HIP stream unless
 given, ``EtpError`` for every non-zero status. Feature matrices are 2-D tensors
 (float32 or bfloat16, all of one call alike) whose rows may be strided
 (``stride(1) == 1``); bias, gamma, beta, row statistics and weight gradients are
-float32.
+float32. The rows' groups are int32. The grouped layer and the gradient list also
+check that their tensors share a device, and launch on that one whichever is current.
 """
 from __future__ import annotations
 
@@ -21,7 +24,13 @@ ETP_ACT_NONE, ETP_ACT_SILU, ETP_ACT_GELU = 0, 1, 2
 
 # every symbol include/etp_dense.h declares
 ABI_SYMBOLS = ("etp_linear", "etp_linear_vjp", "etp_linear_vjp_workspace", "etp_layer_norm", "etp_layer_norm_vjp",
-               "etp_layer_norm_vjp_workspace", "etp_orthogonalize", "etp_orthogonalize_workspace")
+               "etp_layer_norm_vjp_workspace", "etp_orthogonalize", "etp_orthogonalize_workspace",
+               "etp_group_rows", "etp_group_rows_workspace", "etp_grouped_linear", "etp_grouped_linear_vjp",
+               "etp_grouped_linear_vjp_workspace", "etp_grad_norm", "etp_clip_grads", "etp_grad_norm_workspace")
+
+
+class etp_tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 def _declare():
@@ -36,6 +45,15 @@ def _declare():
         "etp_layer_norm_vjp_workspace": [i64, i32, i32, psz],
         "etp_orthogonalize": [i32, i32, i32, i32, vp, i32, vp, f32, vp, vp, sz, vp],
         "etp_orthogonalize_workspace": [i32, i32, i32, i32, psz],
+        "etp_group_rows": [i64, i32, vp, vp, vp, vp, sz, vp],
+        "etp_group_rows_workspace": [i64, i32, psz],
+        "etp_grouped_linear": [i64, i32, vp, vp, i32, i32, i32, vp, i64, vp, vp, i32, vp, i64, vp, i64, vp, i64, vp],
+        "etp_grouped_linear_vjp": [i64, i32, vp, vp, i32, i32, i32, vp, i64, vp, vp, i64, i32, vp, i64, vp, i64, vp,
+                                   vp, u32, vp, sz, vp],
+        "etp_grouped_linear_vjp_workspace": [i64, i32, i32, i32, i32, psz],
+        "etp_grad_norm": [i32, vp, vp, vp, sz, vp],
+        "etp_clip_grads": [i32, vp, f32, vp, vp, vp, sz, vp],
+        "etp_grad_norm_workspace": [i32, vp, psz],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -219,3 +237,156 @@ def etp_orthogonalize(G, X, steps: int = 5, coef=None, eps: float = 1e-7, ws=Non
     c = None if coef is None else (ctypes.c_float * 3)(*coef)
     _check(lib.etp_orthogonalize(n, r, k, code, _dense(G, "G", dt, G.numel()), steps, c, eps,
                                  _dense_matrix(X, "X", dt, r, k, n), wp, wb, _stream(stream, G)), "etp_orthogonalize")
+
+
+def _call(name, device, stream, *args):
+    """One call on the device its tensors live on (a stream belongs to a device, the launch to the current one)."""
+    f = getattr(lib, name)
+    if torch.cuda.current_device() == device.index:
+        return _check(f(*args, _stream_of(stream, device)), name)
+    with torch.cuda.device(device):
+        _check(f(*args, _stream_of(stream, device)), name)
+
+
+def _stream_of(stream, device):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _any_stream(stream)
+
+
+def _share_device(first, *tensors):
+    for t in tensors:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors of one call must share a device, got {first.device} and {t.device}")
+    return first.device
+
+
+def etp_group_rows_workspace(n_rows: int, n_groups: int) -> int:
+    return _bytes("etp_group_rows_workspace", n_rows, n_groups)
+
+
+def etp_group_rows(ids, group_ptr, order, ws=None, stream=None):
+    """group_ptr [G + 1] and order [M], int32: the rows of ids int32 [M] by group, in row order within each, rows whose
+    id is none of 0 .. G - 1 last; ws: etp_group_rows_workspace(M, G) bytes."""
+    M, G, i32 = ids.numel(), group_ptr.numel() - 1, torch.int32
+    wp, wb = _workspace(ws)
+    args = (M, G, _dense(ids, "ids", i32, M), _dense(group_ptr, "group_ptr", i32, G + 1),
+            _dense(order, "order", i32, M), wp, wb)
+    _call("etp_group_rows", _share_device(ids, group_ptr, order, ws), stream, *args)
+
+
+def _groups(group_ptr, order, rows):
+    """(number of groups, pointers of the offsets and of the order)"""
+    G = group_ptr.numel() - 1
+    return G, _dense(group_ptr, "group_ptr", torch.int32, G + 1), _dense(order, "order", torch.int32, rows, True)
+
+
+def etp_grouped_linear(x, W, y, group_ptr, order=None, bias=None, activation: int = ETP_ACT_NONE, residual=None, z=None,
+                       stream=None):
+    """z = x @ W[g] + bias[g], y = act(z) + residual for the rows order[group_ptr[g]:group_ptr[g + 1]] of each group g
+    (order None: the rows themselves). x [M, K], W [G, K, N]; residual, y, z [M, N]; bias float [G, N]. Rows in no group
+    are left alone."""
+    M, K = _matrix(x, "x")
+    N, dt = W.shape[-1], x.dtype
+    code = _code(dt)
+    G, gp, op = _groups(group_ptr, order, M)
+    xp, ldx = _rows(x, "x", dt, M, K)
+    rp, ldr = _rows(residual, "residual", dt, M, N, True)
+    yp, ldy = _rows(y, "y", dt, M, N)
+    zp, ldz = _rows(z, "z", dt, M, N, True)
+    args = (M, G, gp, op, K, N, code, xp, ldx, _dense_matrix(W, "W", dt, K, N, G),
+            _dense(bias, "bias", torch.float32, G * N, True), activation, rp, ldr, yp, ldy, zp, ldz)
+    _call("etp_grouped_linear", _share_device(x, W, y, group_ptr, order, bias, residual, z), stream, *args)
+
+
+def etp_grouped_linear_vjp_workspace(n_rows: int, n_groups: int, n_in: int, n_out: int, dtype=torch.float32) -> int:
+    return _bytes("etp_grouped_linear_vjp_workspace", n_rows, n_groups, n_in, n_out, _code(dtype))
+
+
+def etp_grouped_linear_vjp(x, W, grad_y, group_ptr, order=None, z=None, activation: int = ETP_ACT_NONE, grad_x=None,
+                           grad_W=None, grad_b=None, ws=None, flags: int = 0, stream=None):
+    """VJP of etp_grouped_linear: grad_x [M, K], grad_W float [G, K, N], grad_b float [G, N] (each optional; x may be
+    None without grad_W, W without grad_x); ws: etp_grouped_linear_vjp_workspace(M, G, K, N, dtype) bytes."""
+    M, N = _matrix(grad_y, "grad_y")
+    dt = grad_y.dtype
+    if W is not None:
+        if W.dim() != 3:
+            raise ValueError(f"W must be [groups][rows][cols], got {list(W.shape)}")
+        K = W.shape[1]
+    else:
+        given = x if x is not None else grad_x
+        K = 1 if given is None else _matrix(given, "x" if x is not None else "grad_x")[1]  # (grad_b has no K)
+    code = _code(dt)
+    G, gp, op = _groups(group_ptr, order, M)
+    Wp = _dense_matrix(W, "W", dt, K, N, G, optional=True)
+    xp, ldx = _rows(x, "x", dt, M, K, True)
+    zp, ldz = _rows(z, "z", dt, M, N, True)
+    yp, ldy = _rows(grad_y, "grad_y", dt, M, N)
+    gxp, ldgx = _rows(grad_x, "grad_x", dt, M, K, True)
+    wp, wb = _workspace(ws)
+    f32 = torch.float32
+    args = (M, G, gp, op, K, N, code, xp, ldx, Wp, zp, ldz, activation, yp, ldy, gxp, ldgx,
+            _dense_matrix(grad_W, "grad_W", f32, K, N, G, optional=True),
+            _dense(grad_b, "grad_b", f32, G * N, True), flags, wp, wb)
+    _call("etp_grouped_linear_vjp", _share_device(grad_y, x, W, group_ptr, order, z, grad_x, grad_W, grad_b, ws), stream,
+          *args)
+
+
+class TensorList:
+    """Device tensors (float32 or bfloat16, contiguous, of one device) named once for many calls: the list of
+    etp_grad_norm and etp_clip_grads, or the latter's outputs. It holds the tensors, whose memory must stay where it is
+    (no ``set_`` or ``.data`` in between)."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        n = len(self.tensors)
+        self.items, self.pointers = (etp_tensor * max(n, 1))(), (ctypes.c_void_p * max(n, 1))()
+        self.n, self.shape = n, [(t.dtype, t.numel()) for t in self.tensors]
+        self.device = self.tensors[0].device if n else None
+        spans = []
+        for i, t in enumerate(self.tensors):
+            p = _dense(t, f"tensor {i}", t.dtype, t.numel())
+            self.items[i] = etp_tensor(p, t.numel(), _code(t.dtype))
+            self.pointers[i] = p
+            if t.numel():
+                spans.append((p, p + t.numel() * t.element_size()))
+        _share_device(*self.tensors) if n else None
+        spans.sort()
+        self.apart = all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+
+
+def _tensor_list(tensors):
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def etp_grad_norm_workspace(grads) -> int:
+    """Bytes for etp_grad_norm and etp_clip_grads over grads (a TensorList or tensors)."""
+    g = _tensor_list(grads)
+    return _bytes("etp_grad_norm_workspace", g.n, g.items)
+
+
+def etp_grad_norm(grads, norm, ws=None, stream=None):
+    """norm (float, one element) = the 2-norm of all tensors of grads (a TensorList or tensors) taken as one vector; ws:
+    etp_grad_norm_workspace(grads) bytes."""
+    g = _tensor_list(grads)
+    wp, wb = _workspace(ws)
+    np_ = _dense(norm, "norm", torch.float32, 1)
+    _call("etp_grad_norm", _share_device(norm, ws, *g.tensors[:1]), stream, g.n, g.items, np_, wp, wb)
+
+
+def etp_clip_grads(grads, max_norm: float, out=None, norm=None, ws=None, stream=None):
+    """out[i] = grads[i] * min(1, max_norm / norm) with the norm of etp_grad_norm, which is written to norm (float, one
+    element) when given. out: a TensorList or tensors of the same types and sizes, or None: in place. ws:
+    etp_grad_norm_workspace(grads) bytes."""
+    g = _tensor_list(grads)
+    o = g if out is None else _tensor_list(out)
+    if o.shape != g.shape:
+        raise ValueError("out must hold tensors of the types and sizes of grads")
+    if not o.apart:
+        raise ValueError("the clipped tensors overlap")
+    wp, wb = _workspace(ws)
+    np_ = _dense(norm, "norm", torch.float32, 1, True)
+    first = [t for t in (*g.tensors[:1], *o.tensors[:1], norm, ws) if t is not None]
+    if not first:
+        return
+    _call("etp_clip_grads", _share_device(*first), stream, g.n, g.items, max_norm, o.pointers, np_, wp, wb)

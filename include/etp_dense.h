@@ -143,6 +143,103 @@ ETP_API etp_status etp_orthogonalize(int32_t n_mats, int32_t rows, int32_t cols,
 ETP_API etp_status etp_orthogonalize_workspace(int32_t n_mats, int32_t rows, int32_t cols, int32_t dtype,
                                                size_t *bytes);
 
+/* Rows grouped by a type id (an atom's element, an edge's pair of elements):
+ *   group_ptr[g] = the number of rows with 0 <= ids[r] < g,   g = 0 .. n_groups
+ *   order[s]     = the rows by group, in row order within each (a stable sort);
+ * rows whose id is none of 0 .. n_groups - 1 (padding) are in no group and come
+ * behind, from group_ptr[n_groups] on. ids int32 [n_rows]; group_ptr int32
+ * [n_groups + 1]; order int32 [n_rows]. For the types of a fixed structure this
+ * is done once. (etp_csr_transpose groups edges by source too, in a time that
+ * grows with the square of a long group.) ws: DEVICE, 16-byte aligned, at least
+ * etp_group_rows_workspace() bytes (NULL where that is 0). n_rows = 0 writes
+ * zeros into group_ptr. Errors: INVALID_ARGUMENT (null group_ptr, null ids or
+ * order with n_rows > 0, negative n_rows, n_groups below 1, misaligned
+ * pointers), UNSUPPORTED (n_rows >= 2^31, n_groups >= 2^16), WORKSPACE, HIP. */
+ETP_API etp_status etp_group_rows(int64_t n_rows, int32_t n_groups, const int32_t *ids, int32_t *group_ptr,
+                                  int32_t *order, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace (bytes) of etp_group_rows. Host only. Errors: INVALID_ARGUMENT
+ * (null bytes, negative n_rows, n_groups below 1), UNSUPPORTED. */
+ETP_API etp_status etp_group_rows_workspace(int64_t n_rows, int32_t n_groups, size_t *bytes);
+
+/* Linear layer with a matrix for each group of rows:
+ *   z[r, j] = sum_k x[r, k] W[g, k, j] + bias[g, j],   y[r, j] = act(z[r, j]) + residual[r, j]
+ * for every row r = order[s], group_ptr[g] <= s < group_ptr[g + 1] (order NULL:
+ * r = s, rows that lie in groups). Features stay in the caller's row order.
+ * W [n_groups][n_in][n_out]; bias float [n_groups][n_out] or NULL; everything
+ * else as etp_linear. Rows in no group (before group_ptr[0], behind
+ * group_ptr[n_groups]) are neither read nor written. group_ptr, order: DEVICE
+ * int32, as etp_group_rows writes them, and trusted: a row named twice is written
+ * twice, in any order (an index that is no row is passed over, offsets outside [0,
+ * n_rows] are held to that range). The sizes of the groups are not read back;
+ * empty groups cost next to nothing. Errors: as etp_linear, plus INVALID_ARGUMENT
+ * (null group_ptr, n_groups below 1), UNSUPPORTED (n_groups >= 2^16). */
+ETP_API etp_status etp_grouped_linear(int64_t n_rows, int32_t n_groups, const int32_t *group_ptr,
+                                      const int32_t *order, int32_t n_in, int32_t n_out, int32_t dtype, const void *x,
+                                      int64_t ldx, const void *W, const float *bias, int32_t activation,
+                                      const void *residual, int64_t ldr, void *y, int64_t ldy, void *z, int64_t ldz,
+                                      void *stream);
+
+/* VJP of etp_grouped_linear: with d = grad_y * act'(z), for the rows of each group
+ *   grad_x[r, k]    = sum_j d[r, j] W[g, k, j]         (dtype, pitch ldgx)
+ *   grad_W[g, k, j] = sum_{r in g} x[r, k] d[r, j]     (float [n_groups][n_in][n_out])
+ *   grad_b[g, j]    = sum_{r in g} d[r, j]             (float [n_groups][n_out])
+ * Outputs, flags, z and ws as etp_linear_vjp, with
+ * etp_grouped_linear_vjp_workspace() bytes (needed for grad_W and grad_b). d is a
+ * float also when the features are bf16; without an activation it is grad_y as
+ * stored. Gradients of groups without rows are zero (or left as they are when
+ * accumulating); rows of grad_x in no group are not written. Errors: as
+ * etp_linear_vjp, plus those of etp_grouped_linear. */
+ETP_API etp_status etp_grouped_linear_vjp(int64_t n_rows, int32_t n_groups, const int32_t *group_ptr,
+                                          const int32_t *order, int32_t n_in, int32_t n_out, int32_t dtype,
+                                          const void *x, int64_t ldx, const void *W, const void *z, int64_t ldz,
+                                          int32_t activation, const void *grad_y, int64_t ldgy, void *grad_x,
+                                          int64_t ldgx, float *grad_W, float *grad_b, uint32_t flags, void *ws,
+                                          size_t ws_bytes, void *stream);
+
+/* Workspace (bytes) of etp_grouped_linear_vjp. Host only. Errors: as
+ * etp_linear_vjp_workspace, plus n_groups as etp_grouped_linear. */
+ETP_API etp_status etp_grouped_linear_vjp_workspace(int64_t n_rows, int32_t n_groups, int32_t n_in, int32_t n_out,
+                                                    int32_t dtype, size_t *bytes);
+
+/* One tensor of a list (the list is a HOST array): numel entries of dtype, dense. */
+typedef struct {
+    const void *data; /* DEVICE; may be NULL where numel is 0 */
+    int64_t numel;
+    int32_t dtype; /* etp_dtype */
+} etp_tensor;
+
+/* Norm of all tensors taken as one vector,
+ *   norm = sqrt(sum_i sum_e grads[i][e]^2)
+ * with squares and sums in double and one rounding to float at the end: no
+ * square overflows or vanishes. norm: DEVICE float. It is not finite where an
+ * entry is not (or where the norm is no float). The list is read during the call
+ * only; a captured graph keeps the addresses. n_tensors = 0 gives 0. ws: DEVICE,
+ * 16-byte aligned, at least etp_grad_norm_workspace() bytes. Errors:
+ * INVALID_ARGUMENT (null list with n_tensors > 0, null norm, negative n_tensors
+ * or numel, null data with numel > 0, unknown dtype, misaligned pointers),
+ * UNSUPPORTED (a numel of 2^43 or more), WORKSPACE, HIP. */
+ETP_API etp_status etp_grad_norm(int32_t n_tensors, const etp_tensor *grads, float *norm, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/* Clipping to a largest norm: with norm as above (kept in double),
+ *   out[i][e] = grads[i][e] * (norm <= max_norm ? 1 : max_norm / norm)
+ * rounded once. out: HOST array of DEVICE pointers, each of its tensor's type,
+ * dense, equal to its tensor's data (in place) or apart from every tensor of the
+ * call; NULL: all in place. In place nothing is written when the norm is small
+ * enough. An infinite norm gives zeros (NaN from the infinite entries), a NaN
+ * makes every entry NaN: *norm tells. norm: DEVICE float, written when not NULL.
+ * max_norm: finite, >= 0. ws as etp_grad_norm. Errors: as etp_grad_norm (norm may
+ * be NULL), plus INVALID_ARGUMENT (max_norm, an out[i] that is null with entries
+ * or misaligned). */
+ETP_API etp_status etp_clip_grads(int32_t n_tensors, const etp_tensor *grads, float max_norm, void *const *out,
+                                  float *norm, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace (bytes) of etp_grad_norm and etp_clip_grads for a list; its data
+ * pointers are not looked at. Host only. Errors: INVALID_ARGUMENT (null bytes,
+ * otherwise as etp_grad_norm), UNSUPPORTED. */
+ETP_API etp_status etp_grad_norm_workspace(int32_t n_tensors, const etp_tensor *grads, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif
