@@ -38,7 +38,7 @@ def units():
     """(source, object, extra flags) for every translation unit."""
     out = []
     for name in ("etp_api", "etp_sh", "etp_graph", "etp_mix", "etp_forces", "etp_neighbors", "etp_node_product",
-                 "etp_dense_api", "etp_linear", "etp_layer_norm", "etp_orth", "etp_grouped", "etp_group_rows",
+                 "etp_dense_api", "etp_linear", "etp_layer_norm", "etp_orth", "etp_grouped", "etp_grouped_vjp", "etp_group_rows",
                  "etp_grad_norm"):
         out.append((os.path.join(CSRC, name + ".hip"), os.path.join(BUILD, name + ".o"), []))
     for L in range(5):

@@ -2,12 +2,13 @@
 // scaling to a largest norm.
 //
 // Squares are added in double: no square of a float overflows or vanishes, and
-// what a sum of 2^30 terms loses is far below a float's rounding. A launch
-// carries its tensors' addresses in its arguments (kTableTensors of them: 4 KiB),
+// what a sum of 2^30 terms loses is far below a float's rounding. The tensors are
 // cut into chunks of kChunk entries; a workgroup owns a run of chunks and leaves
 // one partial sum. Whoever needs the norm adds the partial sums in the same fixed
-// order: the scaling launch does so in every workgroup, instead of a launch in
-// between.
+// order: the scaling launch does so in every workgroup, while its first chunk is
+// on its way, instead of a launch in between. Addresses and sizes travel in a
+// launch's arguments (kTableTensors fill the 4 KiB); of more tensors they are
+// written into the workspace first.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -18,26 +19,34 @@
 namespace etp {
 
 constexpr int kChunk = 8192;
-constexpr int kTableTensors = 140;
-constexpr int kMostRuns = 2048;  // workgroups of a launch
+constexpr int kTableTensors = 120;
+constexpr int kMostRuns = 2048;       // workgroups of a launch, and partial sums
+constexpr int kSmallEntries = 32768;  // one workgroup reads and scales so many
+constexpr int kPiece = 512;           // entries a wave of it takes at a time
 
-struct TensorTable {
-    const void *in[kTableTensors];
-    void *out[kTableTensors];
-    int64_t numel[kTableTensors];  // negative: bf16, of -numel entries
-    int first[kTableTensors];      // chunk of the tensor's start
-    int n, chunks, per;            // per: chunks of a workgroup
-    int part0;                     // partial sums of the launches before
+struct TensorEntry {
+    const void *in;
+    void *out;
+    int64_t numel;  // negative: bf16, of -numel entries
+    int64_t first;  // chunk (piece) of the tensor's start
 };
-static_assert(sizeof(TensorTable) <= 4000);
+struct TensorTable {
+    TensorEntry e[kTableTensors];
+};
+static_assert(sizeof(TensorTable) <= 3840);
+
+struct Runs {
+    int64_t chunks, per;  // in all, and of a workgroup
+    int tensors;
+};
 
 // The last tensor that starts at or before a chunk.
-__device__ __forceinline__ int tensor_of(const TensorTable &t, int chunk)
+__device__ __forceinline__ int tensor_of(const TensorEntry *e, int n, int64_t chunk)
 {
-    int lo = 0, hi = t.n;
+    int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (t.first[mid] <= chunk)
+        if (e[mid].first <= chunk)
             lo = mid;
         else
             hi = mid;
@@ -45,7 +54,8 @@ __device__ __forceinline__ int tensor_of(const TensorTable &t, int chunk)
     return lo;
 }
 
-// The sum over a workgroup of 256 threads, in every thread.
+// The sum over a workgroup of Waves waves, in every thread.
+template <int Waves>
 __device__ __forceinline__ double block_sum(double v, double *lds)
 {
 #pragma unroll
@@ -54,61 +64,128 @@ __device__ __forceinline__ double block_sum(double v, double *lds)
     if ((threadIdx.x & 63) == 0)
         lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < Waves; ++w)
+        v += lds[w];
     __syncthreads();
     return v;
 }
 
-template <typename T>
-__device__ __forceinline__ double chunk_squares(const T *p, int n)
-{
-    constexpr int V = kVec<T>;
-    double s = 0.0;
-    int i = threadIdx.x * V;
-#pragma unroll 4
-    for (; i + V <= n; i += 256 * V) {
-        RawVec<T> v;
-        v.load(p + i, V);
+// A thread's share of Entries consecutive entries, Threads threads 16 bytes each in
+// turn, as loaded.
+template <typename T, int Threads, int Entries>
+struct Share {
+    static constexpr int V = kVec<T>, N = Entries / (Threads * V);
+    static_assert(N >= 1 && N * Threads * V == Entries);
+    RawVec<T> v[N];
+    __device__ __forceinline__ void load(const TensorEntry &t, int64_t at, int n, int id)
+    {
+        const T *p = static_cast<const T *>(t.in) + at;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const double x = v.get(k);
-            s = __builtin_fma(x, x, s);
+        for (int k = 0; k < N; ++k) {
+            const int i = (k * Threads + id) * V;
+            v[k].load(p + (i < n ? i : 0), n - i);
         }
     }
-    for (; i < n; ++i) {  // the piece that the end cuts
-        const double x = to_f32(p[i]);
-        s = __builtin_fma(x, x, s);
+    // (entries past the end were loaded as zeros)
+    __device__ __forceinline__ double squares() const
+    {
+        double s = 0.0;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const double x = v[k].get(j);
+                s = __builtin_fma(x, x, s);
+            }
+        return s;
     }
-    return s;
+    // the product with a double, rounded once to float (and once more to bf16)
+    __device__ __forceinline__ void scale(const TensorEntry &t, int64_t at, int n, int id, double by) const
+    {
+        T *p = static_cast<T *>(t.out) + at;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = (k * Threads + id) * V;
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                y[j] = static_cast<float>(v[k].get(j) * by);
+            if (i < n)
+                store_n<V>(p + i, n - i, y);
+        }
+    }
+};
+
+// Where a chunk lies: its tensor, first entry and number of entries.
+template <int Entries>
+struct Place {
+    int64_t at;
+    int n;
+    bool bf16;
+    __device__ __forceinline__ Place(const TensorEntry &t, int64_t chunk)
+    {
+        const int64_t size = t.numel;
+        bf16 = size < 0;
+        at = (chunk - t.first) * Entries;
+        const int64_t rest = (bf16 ? -size : size) - at;
+        n = rest < Entries ? static_cast<int>(rest) : Entries;
+    }
+};
+
+__global__ void __launch_bounds__(128) grad_table_kernel(const TensorTable t, int n, TensorEntry *__restrict__ to)
+{
+    if (static_cast<int>(threadIdx.x) < n)
+        to[threadIdx.x] = t.e[threadIdx.x];
 }
 
-__global__ void __launch_bounds__(256) grad_squares_kernel(const TensorTable t, double *__restrict__ part)
+// In the place of a table that lies in memory.
+struct NoTable {
+    TensorEntry e[1];
+};
+
+template <typename Table>
+__global__ void __launch_bounds__(256)
+    grad_squares_kernel(const Table t, const TensorEntry *__restrict__ far, const Runs r, double *__restrict__ part)
 {
+    const TensorEntry *e = sizeof(Table) == sizeof(NoTable) ? far : t.e;
     __shared__ double lds[4];
-    const int from = blockIdx.x * t.per, stop = from + t.per < t.chunks ? from + t.per : t.chunks;
-    int k = tensor_of(t, from);
+    const int64_t from = blockIdx.x * r.per, stop = from + r.per < r.chunks ? from + r.per : r.chunks;
+    int k = tensor_of(e, r.tensors, from);
     double s = 0.0;
-    for (int c = from; c < stop; ++c) {
-        while (k + 1 < t.n && t.first[k + 1] <= c)
+    for (int64_t c = from; c < stop; ++c) {
+        while (k + 1 < r.tensors && e[k + 1].first <= c)
             ++k;
-        const int64_t at = static_cast<int64_t>(c - t.first[k]) * kChunk, size = t.numel[k];
-        const int64_t rest = (size < 0 ? -size : size) - at;
-        const int n = rest < kChunk ? static_cast<int>(rest) : kChunk;
-        s += size < 0 ? chunk_squares(static_cast<const bf16bits *>(t.in[k]) + at, n)
-                      : chunk_squares(static_cast<const float *>(t.in[k]) + at, n);
+        const Place<kChunk> p(e[k], c);
+        if (p.bf16) {
+            Share<bf16bits, 256, kChunk> v;
+            v.load(e[k], p.at, p.n, threadIdx.x);
+            s += v.squares();
+        } else {
+            Share<float, 256, kChunk> v;
+            v.load(e[k], p.at, p.n, threadIdx.x);
+            s += v.squares();
+        }
     }
-    s = block_sum(s, lds);
+    s = block_sum<4>(s, lds);
     if (threadIdx.x == 0)
-        part[t.part0 + blockIdx.x] = s;
+        part[blockIdx.x] = s;
 }
 
 __device__ __forceinline__ double norm_of_parts(const double *part, int parts, double *lds)
 {
     double s = 0.0;
-    for (int i = threadIdx.x; i < parts; i += 256)
-        s += part[i];
-    return __builtin_sqrt(block_sum(s, lds));
+#pragma unroll
+    for (int k = 0; k < kMostRuns / 256; ++k) {
+        const int i = k * 256 + threadIdx.x;
+        s += i < parts ? part[i] : 0.0;
+    }
+    return __builtin_sqrt(block_sum<4>(s, lds));
 }
+
+// A norm that is not a number makes everything one.
+__device__ __forceinline__ double scale_of(double norm, float max_norm) { return norm <= max_norm ? 1.0 : max_norm / norm; }
 
 __global__ void __launch_bounds__(256) grad_norm_kernel(const double *__restrict__ part, int parts, float *norm)
 {
@@ -118,141 +195,186 @@ __global__ void __launch_bounds__(256) grad_norm_kernel(const double *__restrict
         *norm = static_cast<float>(v);
 }
 
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const T *p, T *o, int n, double scale)
+template <typename Table>
+__global__ void __launch_bounds__(256)
+    grad_scale_kernel(const Table t, const TensorEntry *__restrict__ far, const Runs r, const double *__restrict__ part,
+                      int parts, float max_norm, float *norm)
 {
-    constexpr int V = kVec<T>;
-    int i = threadIdx.x * V;
-#pragma unroll 4
-    for (; i + V <= n; i += 256 * V) {
-        RawVec<T> v;
-        v.load(p + i, V);
-        float y[8];
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            y[k] = static_cast<float>(v.get(k) * scale);
-        store_n<V>(o + i, V, y);
-    }
-    for (; i < n; ++i)
-        o[i] = from_f32<T>(static_cast<float>(to_f32(p[i]) * scale));
-}
-
-__global__ void __launch_bounds__(256) grad_scale_kernel(const TensorTable t, const double *__restrict__ part, int parts,
-                                                         float max_norm, float *norm)
-{
+    const TensorEntry *e = sizeof(Table) == sizeof(NoTable) ? far : t.e;
     __shared__ double lds[4];
-    const double length = norm_of_parts(part, parts, lds);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0)
-        *norm = static_cast<float>(length);
-    // not a number: everything becomes one
-    const double scale = length <= max_norm ? 1.0 : max_norm / length;
     // what was read last is read first: it may still be in the last level of cache
-    const int from = blockIdx.x * t.per, stop = from + t.per < t.chunks ? from + t.per : t.chunks;
-    int k = tensor_of(t, stop - 1);
-    for (int c = stop - 1; c >= from; --c) {
-        while (t.first[k] > c)
+    const int64_t from = blockIdx.x * r.per, stop = from + r.per < r.chunks ? from + r.per : r.chunks;
+    int k = tensor_of(e, r.tensors, stop - 1);
+    double scale = -1.0;
+    auto chunk = [&](auto share, const Place<kChunk> &p) __attribute__((always_inline)) {
+        share.load(e[k], p.at, p.n, threadIdx.x);
+        if (scale < 0.0) {  // once, with the first chunk on its way
+            const double length = norm_of_parts(part, parts, lds);
+            if (norm && blockIdx.x == 0 && threadIdx.x == 0)
+                *norm = static_cast<float>(length);
+            scale = scale_of(length, max_norm);
+        }
+        if (scale != 1.0 || e[k].in != e[k].out)
+            share.scale(e[k], p.at, p.n, threadIdx.x, scale);
+    };
+    for (int64_t c = stop - 1; c >= from; --c) {
+        while (e[k].first > c)
             --k;
-        if (scale == 1.0 && t.in[k] == t.out[k])
-            continue;
-        const int64_t at = static_cast<int64_t>(c - t.first[k]) * kChunk, size = t.numel[k];
-        const int64_t rest = (size < 0 ? -size : size) - at;
-        const int n = rest < kChunk ? static_cast<int>(rest) : kChunk;
-        if (size < 0)
-            chunk_scale(static_cast<const bf16bits *>(t.in[k]) + at, static_cast<bf16bits *>(t.out[k]) + at, n, scale);
+        const Place<kChunk> p(e[k], c);
+        if (p.bf16)
+            chunk(Share<bf16bits, 256, kChunk>(), p);
         else
-            chunk_scale(static_cast<const float *>(t.in[k]) + at, static_cast<float *>(t.out[k]) + at, n, scale);
+            chunk(Share<float, 256, kChunk>(), p);
     }
 }
 
-// Fills the table with the tensors from i on that are not empty; returns the
-// first one that does not fit.
-static int fill_table(TensorTable &t, const GradList &g, int i)
+// Few entries: norm and scaling in one workgroup of 16 waves and one launch. out:
+// whether to scale.
+__global__ void __launch_bounds__(1024)
+    grad_small_kernel(const TensorTable t, const Runs r, int scales, float max_norm, float *norm)
 {
-    t.n = 0;
-    int64_t chunks = 0;
-    for (; i < g.n && t.n < kTableTensors; ++i) {
-        const int64_t numel = g.tensors[i].numel, c = (numel + kChunk - 1) / kChunk;
-        if (numel == 0)
-            continue;
-        if (chunks + c >= (int64_t{1} << 31))
-            break;
-        t.in[t.n] = g.tensors[i].data;
-        t.out[t.n] = g.out ? g.out[i] : const_cast<void *>(g.tensors[i].data);
-        t.numel[t.n] = g.tensors[i].dtype == ETP_BF16 ? -numel : numel;
-        t.first[t.n] = static_cast<int>(chunks);
-        ++t.n;
-        chunks += c;
+    __shared__ double lds[16];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int pieces = static_cast<int>(r.chunks);
+    double s = 0.0;
+    for (int c = wave; c < pieces; c += 16) {
+        const int k = tensor_of(t.e, r.tensors, c);
+        const Place<kPiece> p(t.e[k], c);
+        if (p.bf16) {
+            Share<bf16bits, 64, kPiece> v;
+            v.load(t.e[k], p.at, p.n, lane);
+            s += v.squares();
+        } else {
+            Share<float, 64, kPiece> v;
+            v.load(t.e[k], p.at, p.n, lane);
+            s += v.squares();
+        }
     }
-    t.chunks = static_cast<int>(chunks);
-    t.per = static_cast<int>((chunks + kMostRuns - 1) / kMostRuns);
+    const double length = __builtin_sqrt(block_sum<16>(s, lds));
+    if (norm && threadIdx.x == 0)
+        *norm = static_cast<float>(length);
+    if (!scales)
+        return;
+    const double scale = scale_of(length, max_norm);
+    for (int c = wave; c < pieces; c += 16) {
+        const int k = tensor_of(t.e, r.tensors, c);
+        if (scale == 1.0 && t.e[k].in == t.e[k].out)
+            continue;
+        const Place<kPiece> p(t.e[k], c);
+        if (p.bf16) {
+            Share<bf16bits, 64, kPiece> v;
+            v.load(t.e[k], p.at, p.n, lane);
+            v.scale(t.e[k], p.at, p.n, lane, scale);
+        } else {
+            Share<float, 64, kPiece> v;
+            v.load(t.e[k], p.at, p.n, lane);
+            v.scale(t.e[k], p.at, p.n, lane, scale);
+        }
+    }
+}
+
+// The tensors that are not empty, in chunks of so many entries.
+struct ListSize {
+    int tensors = 0;
+    int64_t entries = 0, chunks = 0;
+};
+static ListSize size_of(const GradList &g, int chunk)
+{
+    ListSize s;
+    for (int i = 0; i < g.n; ++i) {
+        const int64_t n = g.tensors[i].numel;
+        s.tensors += n > 0;
+        s.entries += n;
+        s.chunks += (n + chunk - 1) / chunk;
+    }
+    return s;
+}
+
+// One table's entries from tensor i on; `first` runs on. Returns the tensor behind.
+static int fill_table(TensorTable &t, int &n, const GradList &g, int i, int chunk, int64_t &first)
+{
+    for (n = 0; i < g.n && n < kTableTensors; ++i) {
+        const etp_tensor &x = g.tensors[i];
+        if (x.numel == 0)
+            continue;
+        t.e[n++] = {x.data, g.out ? g.out[i] : const_cast<void *>(x.data), x.dtype == ETP_BF16 ? -x.numel : x.numel, first};
+        first += (x.numel + chunk - 1) / chunk;
+    }
     return i;
 }
 
-static int runs_of(const TensorTable &t) { return t.per ? (t.chunks + t.per - 1) / t.per : 0; }
+static bool is_small(const ListSize &s) { return s.tensors <= kTableTensors && s.entries <= kSmallEntries; }
+
+static Runs runs_of(const ListSize &s) { return {s.chunks, (s.chunks + kMostRuns - 1) / kMostRuns, s.tensors}; }
+
+static int parts_of(const Runs &r) { return r.chunks ? static_cast<int>((r.chunks + r.per - 1) / r.per) : 0; }
 
 size_t grad_norm_workspace_bytes(const GradList &g)
 {
-    size_t parts = 0;
-    TensorTable t;
-    for (int i = 0; i < g.n;) {
-        i = fill_table(t, g, i);
-        parts += runs_of(t);
-    }
-    return sizeof(double) * parts;
+    const ListSize s = size_of(g, kChunk);
+    if (is_small(s))
+        return 0;
+    return sizeof(double) * static_cast<size_t>((parts_of(runs_of(s)) + 1) / 2 * 2) +
+           (s.tensors > kTableTensors ? sizeof(TensorEntry) * static_cast<size_t>(s.tensors) : 0);
 }
 
-static hipError_t squares(const GradList &g, double *part, int *parts, hipStream_t stream)
+// The norm, and with `scales` the scaling.
+static hipError_t launch(const GradList &g, bool scales, float max_norm, float *norm, void *ws, hipStream_t stream)
 {
+    const ListSize s = size_of(g, kChunk);
     TensorTable t;
-    *parts = 0;
-    for (int i = 0; i < g.n;) {
-        i = fill_table(t, g, i);
-        if (t.chunks == 0)
-            continue;
-        t.part0 = *parts;
-        hipLaunchKernelGGL(grad_squares_kernel, dim3(runs_of(t)), dim3(256), 0, stream, t, part);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess)
-            return e;
-        *parts += runs_of(t);
+    int n;
+    int64_t first = 0;
+    if (is_small(s)) {
+        fill_table(t, n, g, 0, kPiece, first);
+        hipLaunchKernelGGL(grad_small_kernel, dim3(1), dim3(1024), 0, stream, t, Runs{first, 1, n}, scales ? 1 : 0, max_norm,
+                           norm);
+        return hipGetLastError();
     }
-    return hipSuccess;
+    const Runs r = runs_of(s);
+    const int parts = parts_of(r);
+    double *part = static_cast<double *>(ws);
+    hipError_t e = hipSuccess;
+    if (s.tensors <= kTableTensors) {
+        fill_table(t, n, g, 0, kChunk, first);
+        hipLaunchKernelGGL(grad_squares_kernel<TensorTable>, dim3(parts), dim3(256), 0, stream, t, nullptr, r, part);
+        e = hipGetLastError();
+        if (e == hipSuccess && scales) {
+            hipLaunchKernelGGL(grad_scale_kernel<TensorTable>, dim3(parts), dim3(256), 0, stream, t, nullptr, r, part,
+                               parts, max_norm, norm);
+            e = hipGetLastError();
+        }
+    } else {
+        TensorEntry *far = reinterpret_cast<TensorEntry *>(part + (parts + 1) / 2 * 2);
+        for (int i = 0, at = 0; i < g.n; at += n) {
+            i = fill_table(t, n, g, i, kChunk, first);
+            hipLaunchKernelGGL(grad_table_kernel, dim3(1), dim3(128), 0, stream, t, n, far + at);
+            if ((e = hipGetLastError()) != hipSuccess)
+                return e;
+        }
+        const NoTable none{};
+        hipLaunchKernelGGL(grad_squares_kernel<NoTable>, dim3(parts), dim3(256), 0, stream, none, far, r, part);
+        e = hipGetLastError();
+        if (e == hipSuccess && scales) {
+            hipLaunchKernelGGL(grad_scale_kernel<NoTable>, dim3(parts), dim3(256), 0, stream, none, far, r, part, parts,
+                               max_norm, norm);
+            e = hipGetLastError();
+        }
+    }
+    if (e != hipSuccess || scales)
+        return e;
+    hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(256), 0, stream, part, parts, norm);
+    return hipGetLastError();
 }
 
 hipError_t launch_grad_norm(const GradList &g, float *norm, void *ws, hipStream_t stream)
 {
-    int parts;
-    const hipError_t e = squares(g, static_cast<double *>(ws), &parts, stream);
-    if (e != hipSuccess)
-        return e;
-    hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(256), 0, stream, static_cast<const double *>(ws), parts, norm);
-    return hipGetLastError();
+    return launch(g, false, 0.f, norm, ws, stream);
 }
 
 hipError_t launch_clip_grads(const GradList &g, float max_norm, float *norm, void *ws, hipStream_t stream)
 {
-    int parts;
-    hipError_t e = squares(g, static_cast<double *>(ws), &parts, stream);
-    if (e != hipSuccess)
-        return e;
-    if (parts == 0) {
-        if (!norm)
-            return hipSuccess;
-        hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(256), 0, stream, static_cast<const double *>(ws), 0, norm);
-        return hipGetLastError();
-    }
-    TensorTable t;
-    for (int i = 0; i < g.n;) {
-        i = fill_table(t, g, i);
-        if (t.chunks == 0)
-            continue;
-        hipLaunchKernelGGL(grad_scale_kernel, dim3(runs_of(t)), dim3(256), 0, stream, t, static_cast<const double *>(ws),
-                           parts, max_norm, norm);
-        if ((e = hipGetLastError()) != hipSuccess)
-            return e;
-        norm = nullptr;  // written once
-    }
-    return hipSuccess;
+    return launch(g, true, max_norm, norm, ws, stream);
 }
 
 }  // namespace etp

@@ -52,7 +52,8 @@ def check_clipped(out, grads, scale):
 
 LISTS = [([1], "f"), ([1], "b"), ([3, 5, 7], "fbf"), ([0, 4, 0], "fbf"), ([8192], "f"), ([8193, 8191], "bf"),
          ([64 * 64, 64, 8 * 64, 64, 64, 64, 64 * 8, 8, 8 * 5 * 64], "f" * 9), ([100003, 17, 250001], "bfb"),
-         ([1 + i % 50 for i in range(400)], "fb" * 200), ([9000 + i for i in range(300)], "fbb" * 100),
+         ([1 + i % 50 for i in range(400)], "fb" * 200), ([300] * 120, "bf" * 60), ([32767, 1], "fb"), ([32768, 1], "fb"),
+         ([511, 512, 513, 1024, 7], "fbfbb"), ([70000] * 121, "f" * 121), ([9000 + i for i in range(300)], "fbb" * 100),
          ([5_000_011, 12_345_678], "fb")]
 
 

@@ -23,7 +23,7 @@ def rows(M=100000, G=4, ids=P, ptr=P, order=P, ws=P, wsb=1 << 40):
     (dict(M=-1), INV), (dict(G=0), INV), (dict(G=-3), INV), (dict(ids=None), INV), (dict(ptr=None), INV),
     (dict(order=None), INV), (dict(ids=P + 2), INV), (dict(ptr=P + 1), INV), (dict(order=P + 2), INV),
     (dict(M=0, ptr=None), INV), (dict(M=1 << 31), UNS), (dict(G=65536), UNS), (dict(ws=None), WS), (dict(ws=P + 8), WS),
-    (dict(wsb=64), WS), (dict(M=1000, G=300, ws=None), WS)])
+    (dict(wsb=64), WS), (dict(M=10000, G=300, ws=None), WS)])
 def test_group_rows_refusals(kw, want):
     assert rows(**kw) == want
 
@@ -66,7 +66,7 @@ def tensors(*items):
     return (dense.etp_tensor * max(1, len(items)))(*(dense.etp_tensor(*i) for i in items))
 
 
-GOOD = [(P, 10, 0), (P + 2, 7, 1), (None, 0, 0)]
+GOOD = [(P, 100000, 0), (P + 2, 7, 1), (None, 0, 0)]
 
 
 def norm(items=GOOD, n=None, out=P, ws=P, wsb=1 << 20, null=False):
@@ -92,7 +92,7 @@ def test_gradient_list_refusals(call, kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(most=-1.0), INV), (dict(most=float("nan")), INV), (dict(most=float("inf")), INV),
     (dict(into=[P, None, None]), INV), (dict(into=[P, P + 1, None]), INV), (dict(into=[P + 2, P, None]), INV),
-    (dict(items=[], out=None), OK), (dict(items=[(None, 0, 1)], out=None, ws=None, into=[None]), OK)])
+    (dict(items=[(P, 3, 0)] * 2, into=[P, None]), INV)])
 def test_clip_refusals(kw, want):
     assert clip(**kw) == want
 
@@ -104,7 +104,8 @@ def test_norm_needs_its_output():
 def test_workspace_sizes():
     assert dense.etp_group_rows_workspace(0, 4) == 0
     assert dense.etp_group_rows_workspace(100, 4) == 0
-    assert dense.etp_group_rows_workspace(100, 300) >= 400
+    assert dense.etp_group_rows_workspace(8192, 300) == 0
+    assert dense.etp_group_rows_workspace(10000, 300) >= 40000
     assert dense.etp_group_rows_workspace(1 << 20, 4) > 0
     assert dense.etp_group_rows_workspace((1 << 31) - 1, 65535) >= 4 * ((1 << 31) - 1)
     assert dense.etp_grouped_linear_vjp_workspace(0, 4, 8, 8) == 0
@@ -121,6 +122,8 @@ def test_workspace_sizes():
     assert dense.lib.etp_grouped_linear_vjp_workspace(1, 1, 1, 1, 0, None) == INV
     b = ctypes.c_size_t()
     assert dense.lib.etp_grad_norm_workspace(0, None, ctypes.byref(b)) == OK and b.value == 0
+    assert dense.lib.etp_grad_norm_workspace(2, tensors((None, 1000, 0), (None, 3, 1)), ctypes.byref(b)) == OK
+    assert b.value == 0
     assert dense.lib.etp_grad_norm_workspace(2, tensors((None, 1 << 20, 0), (None, 3, 1)), ctypes.byref(b)) == OK
     assert b.value > 0 and b.value % 8 == 0
     assert dense.lib.etp_grad_norm_workspace(1, tensors((None, 5, 0)), None) == INV
@@ -158,7 +161,7 @@ def _sized_list(n):
 
 def test_every_launch_is_checked():
     """A refused launch is reported by the call that made it: hipGetLastError follows each launch before the next one."""
-    files = ("etp_grouped.hip", "etp_group_rows.hip", "etp_grad_norm.hip")
+    files = ("etp_grouped.hip", "etp_grouped_vjp.hip", "etp_group_rows.hip", "etp_grad_norm.hip")
     for f in files:
         text = open(os.path.join(CSRC, f)).read()
         launches = [m.end() for m in re.finditer(r"hipLaunchKernelGGL\(", text)]
