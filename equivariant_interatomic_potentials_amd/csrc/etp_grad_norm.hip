@@ -3,7 +3,7 @@
 //
 // Squares are added in double: no square of a float overflows or vanishes, and
 // what a sum of 2^30 terms loses is far below a float's rounding. The tensors are
-// cut into chunks of kChunk entries; a workgroup owns a run of chunks and leaves
+// cut into chunks of kChunk bytes; a workgroup owns a run of chunks and leaves
 // one partial sum. Whoever needs the norm adds the partial sums in the same fixed
 // order: the scaling launch does so in every workgroup, while its first chunk is
 // on its way, instead of a launch in between. Addresses and sizes travel in a
@@ -18,11 +18,11 @@
 
 namespace etp {
 
-constexpr int kChunk = 8192;
+constexpr int kChunk = 16384;         // bytes
 constexpr int kTableTensors = 120;
 constexpr int kMostRuns = 2048;       // workgroups of a launch, and partial sums
 constexpr int kSmallEntries = 32768;  // one workgroup reads and scales so many
-constexpr int kPiece = 512;           // entries a wave of it takes at a time
+constexpr int kPiece = 2048;          // bytes a wave of it takes at a time
 
 struct TensorEntry {
     const void *in;
@@ -40,7 +40,22 @@ struct Runs {
     int tensors;
 };
 
-// The last tensor that starts at or before a chunk.
+// The last tensor that starts at or before a chunk: by halves in the arguments, by 64
+// probes a step in memory, where a step costs a microsecond.
+__device__ __forceinline__ int tensor_in_memory(const TensorEntry *e, int n, int64_t chunk)
+{
+    int first = 0, count = n;
+    for (;;) {
+        const int step = (count + 63) >> 6, i = (threadIdx.x & 63) * step;
+        const bool starts = i < count && e[first + i].first <= chunk;
+        const int k = __builtin_amdgcn_readfirstlane(__popcll(__ballot(starts))) - 1;
+        first += k * step;
+        if (step == 1)
+            return first;
+        count = count - k * step < step ? count - k * step : step;
+    }
+}
+
 __device__ __forceinline__ int tensor_of(const TensorEntry *e, int n, int64_t chunk)
 {
     int lo = 0, hi = n;
@@ -72,65 +87,100 @@ __device__ __forceinline__ double block_sum(double v, double *lds)
     return v;
 }
 
-// A thread's share of Entries consecutive entries, Threads threads 16 bytes each in
-// turn, as loaded.
-template <typename T, int Threads, int Entries>
-struct Share {
-    static constexpr int V = kVec<T>, N = Entries / (Threads * V);
-    static_assert(N >= 1 && N * Threads * V == Entries);
-    RawVec<T> v[N];
-    __device__ __forceinline__ void load(const TensorEntry &t, int64_t at, int n, int id)
-    {
-        const T *p = static_cast<const T *>(t.in) + at;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int i = (k * Threads + id) * V;
-            v[k].load(p + (i < n ? i : 0), n - i);
-        }
-    }
-    // (entries past the end were loaded as zeros)
-    __device__ __forceinline__ double squares() const
-    {
-        double s = 0.0;
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const double x = v[k].get(j);
-                s = __builtin_fma(x, x, s);
-            }
-        return s;
-    }
-    // the product with a double, rounded once to float (and once more to bf16)
-    __device__ __forceinline__ void scale(const TensorEntry &t, int64_t at, int n, int id, double by) const
-    {
-        T *p = static_cast<T *>(t.out) + at;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int i = (k * Threads + id) * V;
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                y[j] = static_cast<float>(v[k].get(j) * by);
-            if (i < n)
-                store_n<V>(p + i, n - i, y);
-        }
-    }
-};
-
-// Where a chunk lies: its tensor, first entry and number of entries.
-template <int Entries>
+// Where a chunk of Bytes lies: its addresses, number of bytes and type. (Copied, not
+// pointed to: of a table in the arguments a pointer would make a copy in memory.)
+template <int Bytes>
 struct Place {
-    int64_t at;
+    const unsigned char *in;
+    unsigned char *out;
     int n;
     bool bf16;
     __device__ __forceinline__ Place(const TensorEntry &t, int64_t chunk)
     {
-        const int64_t size = t.numel;
+        const int64_t size = t.numel, at = (chunk - t.first) * Bytes;
         bf16 = size < 0;
-        at = (chunk - t.first) * Entries;
-        const int64_t rest = (bf16 ? -size : size) - at;
-        n = rest < Entries ? static_cast<int>(rest) : Entries;
+        in = static_cast<const unsigned char *>(t.in) + at;
+        out = static_cast<unsigned char *>(t.out) + at;
+        const int64_t rest = (bf16 ? -2 * size : 4 * size) - at;
+        n = rest < Bytes ? static_cast<int>(rest) : Bytes;
+    }
+};
+
+// A thread's share of a chunk, 16 bytes of every 16 Threads, as loaded; zeros past
+// the end.
+template <int Threads, int Bytes>
+struct Share {
+    static constexpr int N = Bytes / (16 * Threads);
+    static_assert(N >= 1 && N * 16 * Threads == Bytes);
+    u32x4 v[N];
+    __device__ __forceinline__ void load(const Place<Bytes> &p, int id)
+    {
+        const unsigned char *base = p.in;
+        if (p.n == Bytes) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                v[k] = *reinterpret_cast<const u32x4_any *>(base + (k * Threads + id) * 16);
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = (k * Threads + id) * 16;
+            v[k] = load8(reinterpret_cast<const bf16bits *>(base + (i < p.n ? i : 0)), (p.n - i) / 2);
+        }
+    }
+    __device__ __forceinline__ static float half(uint32_t u, int j) { return __uint_as_float(j ? u & 0xFFFF0000u : u << 16); }
+    __device__ __forceinline__ double squares(bool bf16) const
+    {
+        double s = 0.0;
+        if (bf16) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const double x = half(v[k][j >> 1], j & 1);
+                    s = __builtin_fma(x, x, s);
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const double x = __uint_as_float(v[k][j]);
+                    s = __builtin_fma(x, x, s);
+                }
+        }
+        return s;
+    }
+    // the product with a double, rounded once to float (and once more to bf16)
+    __device__ __forceinline__ void scale(const Place<Bytes> &p, int id, double by) const
+    {
+        unsigned char *base = p.out;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = (k * Threads + id) * 16;
+            if (i >= p.n)
+                continue;
+            float y[8];
+            if (p.bf16) {
+                // in float where the scale has a float's digits
+                const float f = static_cast<float>(by);
+                if (by >= 0x1p-100) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        y[j] = half(v[k][j >> 1], j & 1) * f;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        y[j] = static_cast<float>(half(v[k][j >> 1], j & 1) * by);
+                }
+                store8(reinterpret_cast<bf16bits *>(base + i), (p.n - i) / 2, y);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    y[j] = static_cast<float>(__uint_as_float(v[k][j]) * by);
+                store_n<4>(reinterpret_cast<float *>(base + i), (p.n - i) / 4, y);
+            }
+        }
     }
 };
 
@@ -149,24 +199,26 @@ template <typename Table>
 __global__ void __launch_bounds__(256)
     grad_squares_kernel(const Table t, const TensorEntry *__restrict__ far, const Runs r, double *__restrict__ part)
 {
-    const TensorEntry *e = sizeof(Table) == sizeof(NoTable) ? far : t.e;
+    constexpr bool kFar = sizeof(Table) == sizeof(NoTable);
+    const TensorEntry *e = kFar ? far : t.e;
     __shared__ double lds[4];
     const int64_t from = blockIdx.x * r.per, stop = from + r.per < r.chunks ? from + r.per : r.chunks;
-    int k = tensor_of(e, r.tensors, from);
+    int k = kFar ? tensor_in_memory(far, r.tensors, from) : tensor_of(e, r.tensors, from);
+    Place<kChunk> p(e[k], from);
+    Share<256, kChunk> v;
+    v.load(p, threadIdx.x);
     double s = 0.0;
     for (int64_t c = from; c < stop; ++c) {
-        while (k + 1 < r.tensors && e[k + 1].first <= c)
-            ++k;
-        const Place<kChunk> p(e[k], c);
-        if (p.bf16) {
-            Share<bf16bits, 256, kChunk> v;
-            v.load(e[k], p.at, p.n, threadIdx.x);
-            s += v.squares();
-        } else {
-            Share<float, 256, kChunk> v;
-            v.load(e[k], p.at, p.n, threadIdx.x);
-            s += v.squares();
+        // the next chunk is on its way while this one is squared
+        const Share<256, kChunk> now = v;
+        const bool bf16 = p.bf16;
+        if (c + 1 < stop) {
+            while (k + 1 < r.tensors && e[k + 1].first <= c + 1)
+                ++k;
+            p = Place<kChunk>(e[k], c + 1);
+            v.load(p, threadIdx.x);
         }
+        s += now.squares(bf16);
     }
     s = block_sum<4>(s, lds);
     if (threadIdx.x == 0)
@@ -200,36 +252,35 @@ __global__ void __launch_bounds__(256)
     grad_scale_kernel(const Table t, const TensorEntry *__restrict__ far, const Runs r, const double *__restrict__ part,
                       int parts, float max_norm, float *norm)
 {
-    const TensorEntry *e = sizeof(Table) == sizeof(NoTable) ? far : t.e;
+    constexpr bool kFar = sizeof(Table) == sizeof(NoTable);
+    const TensorEntry *e = kFar ? far : t.e;
     __shared__ double lds[4];
     // what was read last is read first: it may still be in the last level of cache
     const int64_t from = blockIdx.x * r.per, stop = from + r.per < r.chunks ? from + r.per : r.chunks;
-    int k = tensor_of(e, r.tensors, stop - 1);
-    double scale = -1.0;
-    auto chunk = [&](auto share, const Place<kChunk> &p) __attribute__((always_inline)) {
-        share.load(e[k], p.at, p.n, threadIdx.x);
-        if (scale < 0.0) {  // once, with the first chunk on its way
-            const double length = norm_of_parts(part, parts, lds);
-            if (norm && blockIdx.x == 0 && threadIdx.x == 0)
-                *norm = static_cast<float>(length);
-            scale = scale_of(length, max_norm);
-        }
-        if (scale != 1.0 || e[k].in != e[k].out)
-            share.scale(e[k], p.at, p.n, threadIdx.x, scale);
-    };
+    int k = kFar ? tensor_in_memory(far, r.tensors, stop - 1) : tensor_of(e, r.tensors, stop - 1);
+    Place<kChunk> p(e[k], stop - 1);
+    Share<256, kChunk> v;
+    v.load(p, threadIdx.x);
+    const double length = norm_of_parts(part, parts, lds);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0)
+        *norm = static_cast<float>(length);
+    const double scale = scale_of(length, max_norm);
     for (int64_t c = stop - 1; c >= from; --c) {
-        while (e[k].first > c)
-            --k;
-        const Place<kChunk> p(e[k], c);
-        if (p.bf16)
-            chunk(Share<bf16bits, 256, kChunk>(), p);
-        else
-            chunk(Share<float, 256, kChunk>(), p);
+        const Share<256, kChunk> now = v;
+        const Place<kChunk> here = p;
+        if (c > from) {
+            while (e[k].first > c - 1)
+                --k;
+            p = Place<kChunk>(e[k], c - 1);
+            v.load(p, threadIdx.x);
+        }
+        if (scale != 1.0 || here.in != here.out)
+            now.scale(here, threadIdx.x, scale);
     }
 }
 
-// Few entries: norm and scaling in one workgroup of 16 waves and one launch. out:
-// whether to scale.
+// Few entries: norm and (where asked for) scaling in one workgroup of 16 waves and
+// one launch.
 __global__ void __launch_bounds__(1024)
     grad_small_kernel(const TensorTable t, const Runs r, int scales, float max_norm, float *norm)
 {
@@ -238,17 +289,10 @@ __global__ void __launch_bounds__(1024)
     const int pieces = static_cast<int>(r.chunks);
     double s = 0.0;
     for (int c = wave; c < pieces; c += 16) {
-        const int k = tensor_of(t.e, r.tensors, c);
-        const Place<kPiece> p(t.e[k], c);
-        if (p.bf16) {
-            Share<bf16bits, 64, kPiece> v;
-            v.load(t.e[k], p.at, p.n, lane);
-            s += v.squares();
-        } else {
-            Share<float, 64, kPiece> v;
-            v.load(t.e[k], p.at, p.n, lane);
-            s += v.squares();
-        }
+        const Place<kPiece> p(t.e[tensor_of(t.e, r.tensors, c)], c);
+        Share<64, kPiece> v;
+        v.load(p, lane);
+        s += v.squares(p.bf16);
     }
     const double length = __builtin_sqrt(block_sum<16>(s, lds));
     if (norm && threadIdx.x == 0)
@@ -257,40 +301,39 @@ __global__ void __launch_bounds__(1024)
         return;
     const double scale = scale_of(length, max_norm);
     for (int c = wave; c < pieces; c += 16) {
-        const int k = tensor_of(t.e, r.tensors, c);
-        if (scale == 1.0 && t.e[k].in == t.e[k].out)
+        const Place<kPiece> p(t.e[tensor_of(t.e, r.tensors, c)], c);
+        if (scale == 1.0 && p.in == p.out)
             continue;
-        const Place<kPiece> p(t.e[k], c);
-        if (p.bf16) {
-            Share<bf16bits, 64, kPiece> v;
-            v.load(t.e[k], p.at, p.n, lane);
-            v.scale(t.e[k], p.at, p.n, lane, scale);
-        } else {
-            Share<float, 64, kPiece> v;
-            v.load(t.e[k], p.at, p.n, lane);
-            v.scale(t.e[k], p.at, p.n, lane, scale);
-        }
+        Share<64, kPiece> v;
+        v.load(p, lane);
+        v.scale(p, lane, scale);
     }
 }
 
-// The tensors that are not empty, in chunks of so many entries.
+static int64_t chunks_of(const etp_tensor &x, int bytes)
+{
+    const int64_t each = bytes / (x.dtype == ETP_BF16 ? 2 : 4);
+    return (x.numel + each - 1) / each;
+}
+
+// The tensors that are not empty, in chunks.
 struct ListSize {
     int tensors = 0;
     int64_t entries = 0, chunks = 0;
 };
-static ListSize size_of(const GradList &g, int chunk)
+static ListSize size_of(const GradList &g)
 {
     ListSize s;
     for (int i = 0; i < g.n; ++i) {
-        const int64_t n = g.tensors[i].numel;
-        s.tensors += n > 0;
-        s.entries += n;
-        s.chunks += (n + chunk - 1) / chunk;
+        s.tensors += g.tensors[i].numel > 0;
+        s.entries += g.tensors[i].numel;
+        s.chunks += chunks_of(g.tensors[i], kChunk);
     }
     return s;
 }
 
-// One table's entries from tensor i on; `first` runs on. Returns the tensor behind.
+// One table's entries from tensor i on, in chunks of so many bytes; `first` runs on.
+// Returns the tensor behind.
 static int fill_table(TensorTable &t, int &n, const GradList &g, int i, int chunk, int64_t &first)
 {
     for (n = 0; i < g.n && n < kTableTensors; ++i) {
@@ -298,7 +341,7 @@ static int fill_table(TensorTable &t, int &n, const GradList &g, int i, int chun
         if (x.numel == 0)
             continue;
         t.e[n++] = {x.data, g.out ? g.out[i] : const_cast<void *>(x.data), x.dtype == ETP_BF16 ? -x.numel : x.numel, first};
-        first += (x.numel + chunk - 1) / chunk;
+        first += chunks_of(x, chunk);
     }
     return i;
 }
@@ -311,7 +354,7 @@ static int parts_of(const Runs &r) { return r.chunks ? static_cast<int>((r.chunk
 
 size_t grad_norm_workspace_bytes(const GradList &g)
 {
-    const ListSize s = size_of(g, kChunk);
+    const ListSize s = size_of(g);
     if (is_small(s))
         return 0;
     return sizeof(double) * static_cast<size_t>((parts_of(runs_of(s)) + 1) / 2 * 2) +
@@ -321,7 +364,7 @@ size_t grad_norm_workspace_bytes(const GradList &g)
 // The norm, and with `scales` the scaling.
 static hipError_t launch(const GradList &g, bool scales, float max_norm, float *norm, void *ws, hipStream_t stream)
 {
-    const ListSize s = size_of(g, kChunk);
+    const ListSize s = size_of(g);
     TensorTable t;
     int n;
     int64_t first = 0;

@@ -366,64 +366,75 @@ __device__ __forceinline__ void store_sums(const GroupedPanelArgs &p, int64_t g,
         }
 }
 
-// Adds the parts of the groups that cross runs, 256 entries a workgroup, four a
-// lane, every wave a quarter of the parts in order; and zeroes the gradients of
-// groups without rows. Where there are few groups, row y of the grid is group y;
-// else rows up to runs - 1 are the boundaries between runs, and a boundary stands
-// for the group that crosses it if that crosses no earlier one, and the other rows
-// look for groups without rows (25 groups in 512 runs by boundaries: 18 us, of
-// which most find their group and leave).
+// Adds the parts of the groups that cross runs, kJoin entries a workgroup, four a
+// lane at a time, every wave a quarter of the parts in order; and zeroes the
+// gradients of groups without rows. Where there are few groups, row y of the grid is
+// group y; else rows up to runs - 1 are the boundaries between runs, and a boundary
+// stands for the group that crosses it if that crosses no earlier one, and the other
+// rows look for groups without rows (25 groups in 512 runs by boundaries: 18 us, of
+// which most find their group and leave; by groups 5).
+constexpr int kJoin = 1024;
 __global__ void __launch_bounds__(256) grouped_join_kernel(const GroupedPanelArgs p, const int shift, const int by_group)
 {
     __shared__ float lds[3][64][4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + 4 * lane;
-    const float none[4] = {0.f, 0.f, 0.f, 0.f};
+    const int64_t from = static_cast<int64_t>(blockIdx.x) * kJoin, stop = from + kJoin < p.set ? from + kJoin : p.set;
+    auto zero = [&](int g) {
+        const float none[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t i = from + 4 * threadIdx.x; i < stop; i += 1024)
+            store_sums(p, g, i, none, false);
+    };
     int g = blockIdx.y;
     if (!by_group) {
         const int bounds = p.runs - 1, y = blockIdx.y;
         if (y >= bounds) {
-            for (g = (y - bounds) * 4 + wave; g < p.gr.n; g += 4 * (gridDim.y - bounds))
+            for (g = y - bounds; g < p.gr.n; g += gridDim.y - bounds)
                 if (group_start(p.gr, g + 1) <= group_start(p.gr, g))
-                    store_sums(p, g, i, none, false);
+                    zero(g);
             return;
         }
         g = group_of_tile(p.gr, shift, (y + 1) * p.per);
     }
     const int begin = group_start(p.gr, g), end = group_start(p.gr, g + 1);
     if (end <= begin) {
-        if (by_group && !p.v.accumulate && wave == 0)
-            store_sums(p, g, i, none, false);
+        if (by_group && !p.v.accumulate)
+            zero(g);
         return;
     }
     const int first = (begin >> shift) + g, last = first + ((end - begin - 1) >> shift);
     const int run0 = first / p.per, run1 = last / p.per;
     if (run0 == run1 || (!by_group && run0 != static_cast<int>(blockIdx.y)))
         return;
-    const float *part = static_cast<const float *>(p.v.ws) + i;
-    const int valid = p.set - i < 4 ? static_cast<int>(p.set - i) : 4;
-    float v[8] = {0.f, 0.f, 0.f, 0.f};
-    if (valid > 0)
-        for (int r = run0 + wave; r <= run1; r += 4) {
-            float u[8];
-            load_n<4>(part + (2 * static_cast<int64_t>(r) + (r == run0 ? 1 : 0)) * p.set, valid, u);
+    for (int64_t i0 = from; i0 < stop; i0 += 256) {
+        const int64_t i = i0 + 4 * lane;
+        const float *part = static_cast<const float *>(p.v.ws) + i;
+        const int valid = stop - i < 4 ? static_cast<int>(stop - i) : 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (valid > 0) {
+#pragma unroll 4
+            for (int r = run0 + wave; r <= run1; r += 4) {
+                float u[8];
+                load_n<4>(part + (2 * static_cast<int64_t>(r) + (r == run0 ? 1 : 0)) * p.set, valid, u);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] += u[k];
+            }
+        }
+        if (i0 > from)
+            lds_barrier();  // the sums before have been read
+        if (wave > 0) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                v[k] += u[k];
+                lds[wave - 1][lane][k] = v[k];
         }
-    if (wave > 0) {
+        lds_barrier();
+        if (wave == 0 && valid > 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            lds[wave - 1][lane][k] = v[k];
+            for (int k = 0; k < 4; ++k)
+                v[k] = (v[k] + lds[0][lane][k]) + (lds[1][lane][k] + lds[2][lane][k]);
+            store_sums(p, g, i, v, p.v.accumulate);
+        }
     }
-    lds_barrier();
-    if (wave > 0)
-        return;
-    float sum[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        sum[k] = (v[k] + lds[0][lane][k]) + (lds[1][lane][k] + lds[2][lane][k]);
-    store_sums(p, g, i, sum, p.v.accumulate);
 }
 
 // How a VJP call is cut: as the linear layer's, in one panel kernel where K and N
@@ -590,11 +601,11 @@ static hipError_t grouped_vjp(const GroupedLinearVjpArgs &ga, hipStream_t stream
         return e;
     const bool by_group = gr.n <= 4 * p.runs;
     // groups without rows are looked for by up to 1024 rows of workgroups
-    const int rest = a.accumulate ? 0 : gr.n < 4096 ? (gr.n + 3) / 4 : 1024;
+    const int rest = a.accumulate ? 0 : gr.n < 1024 ? gr.n : 1024;
     const int rows = by_group ? gr.n : p.runs - 1 + rest;
     if (rows == 0)
         return hipSuccess;
-    hipLaunchKernelGGL(grouped_join_kernel, dim3(static_cast<unsigned>((set + 255) / 256), rows), dim3(256), 0, stream, p,
+    hipLaunchKernelGGL(grouped_join_kernel, dim3(static_cast<unsigned>((set + kJoin - 1) / kJoin), rows), dim3(256), 0, stream, p,
                        v.shift, by_group ? 1 : 0);
     return hipGetLastError();
 }
