@@ -34,11 +34,11 @@ struct GroupedShape {
     int px, pd, waves, sx, sd, bufs, rows, shift, lds, per_cu;
     constexpr GroupedShape(bool bf16, int kc, int nc, bool plain)
         : px(bf16 ? 1 : 3), pd(bf16 && plain ? 1 : 3),
-          waves(bf16 ? (kc == 4 && nc > 1 ? 8 : 4) : (kc == 4 || nc == 4 ? 8 : 4)), sx(32 * kc + 8), sd(32 * nc + 8),
-          bufs(waves == 8 && !(bf16 && nc == 2) ? 2 : 1),
-          rows(2 * bufs * 64 * (px * sx + pd * sd) <= 144 * 1024 ? 64 : 32), shift(rows == 64 ? 6 : 5),
+          waves(bf16 ? (kc == 4 && nc > 1 ? 8 : 4) : (kc == 4 || (nc == 4 && !plain) ? 8 : 4)), sx(32 * kc + 8), sd(32 * nc + 8),
+          bufs(waves == 8 ? 2 : 1),
+          rows(!bf16 && waves == 4 && nc == 4 ? 32 : 2 * bufs * 64 * (px * sx + pd * sd) <= 144 * 1024 ? 64 : 32), shift(rows == 64 ? 6 : 5),
           lds(2 * bufs * rows * (px * sx + pd * sd)),
-          per_cu(waves == 8 ? 3 - bufs : 160 * 1024 / lds < 3 ? 160 * 1024 / lds : 3)
+          per_cu(waves == 8 ? 1 : (bf16 && kc == 4) || nc == 4 ? 2 : 160 * 1024 / lds < 3 ? 160 * 1024 / lds : 3)
     {
     }
 };
@@ -234,17 +234,23 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
         }
     };
 
-    TileWalk at;
+    // the panel whose products come next, and the two after it; rows name their rows.
+    // Values are fetched one panel ahead (two with two buffers), indexes one more
+    TileWalk at, then, after;
     at.start(p.gr, S.shift, from, stop);
     if (at.n == 0)
         return;  // the whole workgroup
-    int rows = row_of_slot(p.gr, at.slot + lane, lane < at.n);
+    auto rows_of = [&](const TileWalk &w) { return row_of_slot(p.gr, w.slot + lane, lane < w.n); };
+    int rows = rows_of(at);
     fetch(rows);
-    // the panel after it: its rows' indexes are on their way one panel ahead
-    TileWalk then = at;
+    then = at;
     then.next(p.gr, S.shift, stop);
-    int rows_then = row_of_slot(p.gr, then.slot + lane, lane < then.n);
-    while (at.n > 0) {
+    int rows_then = rows_of(then);
+    after = then;
+    if (then.n > 0)
+        after.next(p.gr, S.shift, stop);
+    int rows_after = rows_of(after);
+    while (at.n > 0) {  // a group; the registers hold its first panel
         const int g = at.g;
         const bool whole = at.first_tile(S.shift) >= from && at.last_tile(S.shift) < stop;
         const int set = 2 * s + (at.first_tile(S.shift) >= from ? 1 : 0);
@@ -273,34 +279,37 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
         if constexpr (S.bufs == 2) {
             lds_barrier();  // of the group before: its sums or its last panel
             put(lds);
-        }
-        for (;;) {
-            // `rows` names the panel in LDS (or about to be), `rows_then` the next
-            const bool more = then.n > 0, same = more && then.g == g;
-            int rows_last = rows_then;
-            if constexpr (S.bufs == 1)
-                put(lds);
-            if (more) {
+            if (then.n > 0)
                 fetch(rows_then);
-                at = then;
-                then.next(p.gr, S.shift, stop);
-                rows_then = row_of_slot(p.gr, then.slot + lane, lane < then.n);
-            } else {
-                at.n = 0;
+        }
+        for (bool same = true; same;) {
+            same = then.n > 0 && then.g == g;
+            if constexpr (S.bufs == 1) {
+                put(lds);
+                if (then.n > 0)
+                    fetch(rows_then);
             }
             lds_barrier();  // the panel's parts are seen by every wave
-            products(lds + buf * kBuf, rows);
-            rows = rows_last;
             if constexpr (S.bufs == 2) {
+                // the other buffer was last read before this barrier
                 if (same) {
-                    buf ^= 1;
-                    put(lds + buf * kBuf);  // was last read before this panel's barrier
+                    put(lds + (buf ^ 1) * kBuf);
+                    if (after.n > 0)
+                        fetch(rows_after);
                 }
-            } else {
-                lds_barrier();  // the next panel overwrites the rows
             }
-            if (!same)
-                break;
+            products(lds + buf * kBuf, rows);
+            buf ^= S.bufs - 1;
+            at = then;
+            rows = rows_then;
+            then = after;
+            rows_then = rows_after;
+            if (then.n > 0) {
+                after.next(p.gr, S.shift, stop);
+                rows_after = rows_of(after);
+            }
+            if constexpr (S.bufs == 1)
+                lds_barrier();  // the next panel overwrites the rows
         }
         // the group's sums
         float *gw = nullptr, *gbias = nullptr;
@@ -366,19 +375,18 @@ __device__ __forceinline__ void store_sums(const GroupedPanelArgs &p, int64_t g,
         }
 }
 
-// Adds the parts of the groups that cross runs, kJoin entries a workgroup, four a
+// Adds the parts of the groups that cross runs, `span` entries a workgroup, four a
 // lane at a time, every wave a quarter of the parts in order; and zeroes the
 // gradients of groups without rows. Where there are few groups, row y of the grid is
 // group y; else rows up to runs - 1 are the boundaries between runs, and a boundary
 // stands for the group that crosses it if that crosses no earlier one, and the other
 // rows look for groups without rows (25 groups in 512 runs by boundaries: 18 us, of
 // which most find their group and leave; by groups 5).
-constexpr int kJoin = 1024;
-__global__ void __launch_bounds__(256) grouped_join_kernel(const GroupedPanelArgs p, const int shift, const int by_group)
+__global__ void __launch_bounds__(256) grouped_join_kernel(const GroupedPanelArgs p, const int shift, const int by_group, const int span)
 {
     __shared__ float lds[3][64][4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t from = static_cast<int64_t>(blockIdx.x) * kJoin, stop = from + kJoin < p.set ? from + kJoin : p.set;
+    const int64_t from = static_cast<int64_t>(blockIdx.x) * span, stop = from + span < p.set ? from + span : p.set;
     auto zero = [&](int g) {
         const float none[4] = {0.f, 0.f, 0.f, 0.f};
         for (int64_t i = from + 4 * threadIdx.x; i < stop; i += 1024)
@@ -447,21 +455,14 @@ struct GroupedCut {
     size_t d_bytes, part_bytes;
 };
 
-static GroupedCut grouped_cut(int64_t M, int G, int K, int N, bool bf16, bool plain)
+// Runs for a tile size and a number of workgroups that run at once: as many as those
+// (one more would double the time), or over up to four rounds where that fills them
+// better by a tenth.
+static void cut_runs(GroupedCut &v, int64_t M, int G, int K, int N, int shift, int per_cu)
 {
-    GroupedCut v{};
-    auto chunks = [](int n) { return n <= 32 ? 1 : n <= 64 ? 2 : 4; };
-    v.kc = chunks(K);
-    v.nc = chunks(N);
-    v.nkb = (K + 127) / 128;
-    v.nnb = (N + 127) / 128;
-    v.fused = K <= 128 && N <= 128;
-    const GroupedShape shape(bf16, v.kc, v.nc, plain);
-    v.shift = shape.shift;
-    v.tiles = static_cast<int>((M >> v.shift) + G);
-    // as many runs as run at once (one more would double the time), or over up to
-    // four rounds where that fills them better by a tenth
-    const int64_t blocks = static_cast<int64_t>(v.nkb) * v.nnb, room = static_cast<int64_t>(kComputeUnits) * shape.per_cu;
+    v.shift = shift;
+    v.tiles = static_cast<int>((M >> shift) + G);
+    const int64_t blocks = static_cast<int64_t>(v.nkb) * v.nnb, room = static_cast<int64_t>(kComputeUnits) * per_cu;
     int64_t s = 0, rounds = 1;
     for (int64_t n = 1; n <= 4; ++n) {
         const int64_t t = n * room / blocks;
@@ -474,10 +475,23 @@ static GroupedCut grouped_cut(int64_t M, int G, int K, int N, bool bf16, bool pl
     s = s < 1 ? 1 : s;
     v.per = static_cast<int>((v.tiles + s - 1) / s);
     v.runs = (v.tiles + v.per - 1) / v.per;
-    v.keep_d = K > 128 && N > 128 && !plain;
-    v.d_bytes = v.keep_d ? (sizeof(float) * static_cast<size_t>(M) * N + 15) / 16 * 16 : 0;
     v.part_bytes = sizeof(float) * 2 * static_cast<size_t>(v.runs) * (static_cast<size_t>(K) + 1) * N;
     v.part_bytes = (v.part_bytes + 15) / 16 * 16;
+}
+
+static GroupedCut grouped_cut(int64_t M, int G, int K, int N, bool bf16, bool plain)
+{
+    GroupedCut v{};
+    auto chunks = [](int n) { return n <= 32 ? 1 : n <= 64 ? 2 : 4; };
+    v.kc = chunks(K);
+    v.nc = chunks(N);
+    v.nkb = (K + 127) / 128;
+    v.nnb = (N + 127) / 128;
+    v.fused = K <= 128 && N <= 128;
+    const GroupedShape shape(bf16, v.kc, v.nc, plain);
+    cut_runs(v, M, G, K, N, shape.shift, shape.per_cu);
+    v.keep_d = K > 128 && N > 128 && !plain;
+    v.d_bytes = v.keep_d ? (sizeof(float) * static_cast<size_t>(M) * N + 15) / 16 * 16 : 0;
     return v;
 }
 
@@ -486,11 +500,10 @@ size_t grouped_linear_vjp_workspace_bytes(int64_t M, int G, int K, int N, bool b
     if (M == 0)
         return 0;
     size_t most = 0;
+    auto take = [&](const GroupedCut &v) { most = v.d_bytes + v.part_bytes > most ? v.d_bytes + v.part_bytes : most; };
     for (const bool plain : {false, true}) {
-        const GroupedCut v = grouped_cut(M, G, K, N, bf16, plain);
-        const size_t all = v.d_bytes + v.part_bytes, bias = grouped_cut(M, G, 1, N, bf16, plain).part_bytes;
-        most = all > most ? all : most;
-        most = bias > most ? bias : most;
+        take(grouped_cut(M, G, K, N, bf16, plain));
+        take(grouped_cut(M, G, 1, N, bf16, plain));  // the bias gradient alone
     }
     return most;
 }
@@ -550,6 +563,22 @@ __global__ void __launch_bounds__(256) grouped_slope_kernel(const LinearVjpArgs 
     }
 }
 
+static hipError_t launch_join(const GroupedPanelArgs &p, int shift, hipStream_t stream)
+{
+    const int n = p.gr.n;
+    const bool by_group = n <= 4 * p.runs;
+    // groups without rows are looked for by up to 1024 rows of workgroups
+    const int rest = p.v.accumulate ? 0 : n < 1024 ? n : 1024;
+    const int rows = by_group ? n : p.runs - 1 + rest;
+    if (rows == 0)
+        return hipSuccess;
+    // (more entries a workgroup where most workgroups would only find nothing to do)
+    const int span = p.set * rows <= (1 << 22) ? 256 : 1024;
+    hipLaunchKernelGGL(grouped_join_kernel, dim3(static_cast<unsigned>((p.set + span - 1) / span), rows), dim3(256), 0,
+                       stream, p, shift, by_group ? 1 : 0, span);
+    return hipGetLastError();
+}
+
 template <typename T>
 static hipError_t grouped_vjp(const GroupedLinearVjpArgs &ga, hipStream_t stream)
 {
@@ -597,17 +626,7 @@ static hipError_t grouped_vjp(const GroupedLinearVjpArgs &ga, hipStream_t stream
         if (set > 0)
             e = plain ? panel_by_shape<T, true>(p, v, stream) : panel_by_shape<T, false>(p, v, stream);
     }
-    if (e != hipSuccess || set == 0)
-        return e;
-    const bool by_group = gr.n <= 4 * p.runs;
-    // groups without rows are looked for by up to 1024 rows of workgroups
-    const int rest = a.accumulate ? 0 : gr.n < 1024 ? gr.n : 1024;
-    const int rows = by_group ? gr.n : p.runs - 1 + rest;
-    if (rows == 0)
-        return hipSuccess;
-    hipLaunchKernelGGL(grouped_join_kernel, dim3(static_cast<unsigned>((set + kJoin - 1) / kJoin), rows), dim3(256), 0, stream, p,
-                       v.shift, by_group ? 1 : 0);
-    return hipGetLastError();
+    return e == hipSuccess && set > 0 ? launch_join(p, v.shift, stream) : e;
 }
 
 hipError_t launch_grouped_linear_vjp(const GroupedLinearVjpArgs &a, hipStream_t stream)
