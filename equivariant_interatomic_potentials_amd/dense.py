@@ -239,26 +239,35 @@ def etp_orthogonalize(G, X, steps: int = 5, coef=None, eps: float = 1e-7, ws=Non
                                  _dense_matrix(X, "X", dt, r, k, n), wp, wb, _stream(stream, G)), "etp_orthogonalize")
 
 
-def _call(name, device, stream, *args):
-    """One call on the device its tensors live on (a stream belongs to a device, the launch to the current one)."""
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(name, device, stream, args):
+    """One call on the device (its number) its tensors live on: a stream belongs to a device, the launch to the current
+    one."""
     f = getattr(lib, name)
-    if torch.cuda.current_device() == device.index:
-        return _check(f(*args, _stream_of(stream, device)), name)
-    with torch.cuda.device(device):
-        _check(f(*args, _stream_of(stream, device)), name)
+    if _current_device() == device:
+        st = f(*args, _stream_of(stream, device))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, _stream_of(stream, device))
+    if st:
+        _check(st, name)
 
 
 def _stream_of(stream, device):
     if stream is None and _raw_stream is not None:
-        return _raw_stream(device.index)
+        return _raw_stream(device)
     return _any_stream(stream)
 
 
 def _share_device(first, *tensors):
+    """The number of the tensors' device."""
+    device = first.get_device()
     for t in tensors:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != device:
             raise ValueError(f"tensors of one call must share a device, got {first.device} and {t.device}")
-    return first.device
+    return device
 
 
 def etp_group_rows_workspace(n_rows: int, n_groups: int) -> int:
@@ -272,7 +281,7 @@ def etp_group_rows(ids, group_ptr, order, ws=None, stream=None):
     wp, wb = _workspace(ws)
     args = (M, G, _dense(ids, "ids", i32, M), _dense(group_ptr, "group_ptr", i32, G + 1),
             _dense(order, "order", i32, M), wp, wb)
-    _call("etp_group_rows", _share_device(ids, group_ptr, order, ws), stream, *args)
+    _call("etp_group_rows", _share_device(ids, group_ptr, order, ws), stream, args)
 
 
 def _groups(group_ptr, order, rows):
@@ -296,7 +305,7 @@ def etp_grouped_linear(x, W, y, group_ptr, order=None, bias=None, activation: in
     zp, ldz = _rows(z, "z", dt, M, N, True)
     args = (M, G, gp, op, K, N, code, xp, ldx, _dense_matrix(W, "W", dt, K, N, G),
             _dense(bias, "bias", torch.float32, G * N, True), activation, rp, ldr, yp, ldy, zp, ldz)
-    _call("etp_grouped_linear", _share_device(x, W, y, group_ptr, order, bias, residual, z), stream, *args)
+    _call("etp_grouped_linear", _share_device(x, W, y, group_ptr, order, bias, residual, z), stream, args)
 
 
 def etp_grouped_linear_vjp_workspace(n_rows: int, n_groups: int, n_in: int, n_out: int, dtype=torch.float32) -> int:
@@ -329,7 +338,7 @@ def etp_grouped_linear_vjp(x, W, grad_y, group_ptr, order=None, z=None, activati
             _dense_matrix(grad_W, "grad_W", f32, K, N, G, optional=True),
             _dense(grad_b, "grad_b", f32, G * N, True), flags, wp, wb)
     _call("etp_grouped_linear_vjp", _share_device(grad_y, x, W, group_ptr, order, z, grad_x, grad_W, grad_b, ws), stream,
-          *args)
+          args)
 
 
 class TensorList:
@@ -342,7 +351,6 @@ class TensorList:
         n = len(self.tensors)
         self.items, self.pointers = (etp_tensor * max(n, 1))(), (ctypes.c_void_p * max(n, 1))()
         self.n, self.shape = n, [(t.dtype, t.numel()) for t in self.tensors]
-        self.device = self.tensors[0].device if n else None
         spans = []
         for i, t in enumerate(self.tensors):
             p = _dense(t, f"tensor {i}", t.dtype, t.numel())
@@ -371,7 +379,7 @@ def etp_grad_norm(grads, norm, ws=None, stream=None):
     g = _tensor_list(grads)
     wp, wb = _workspace(ws)
     np_ = _dense(norm, "norm", torch.float32, 1)
-    _call("etp_grad_norm", _share_device(norm, ws, *g.tensors[:1]), stream, g.n, g.items, np_, wp, wb)
+    _call("etp_grad_norm", _share_device(norm, ws, *g.tensors[:1]), stream, (g.n, g.items, np_, wp, wb))
 
 
 def etp_clip_grads(grads, max_norm: float, out=None, norm=None, ws=None, stream=None):
@@ -389,4 +397,4 @@ def etp_clip_grads(grads, max_norm: float, out=None, norm=None, ws=None, stream=
     first = [t for t in (*g.tensors[:1], *o.tensors[:1], norm, ws) if t is not None]
     if not first:
         return
-    _call("etp_clip_grads", _share_device(*first), stream, g.n, g.items, max_norm, o.pointers, np_, wp, wb)
+    _call("etp_clip_grads", _share_device(*first), stream, (g.n, g.items, max_norm, o.pointers, np_, wp, wb))
