@@ -1,6 +1,5 @@
 // etp_grouped.hip -- the linear layer with a matrix for each group of rows (an
-// element, a pair of elements, an expert), forward and input
-// gradient.
+// element, a pair of elements, an expert), forward and input gradient.
 #include "etp_grouped.hpp"
 
 namespace etp {
@@ -18,15 +17,19 @@ __device__ __forceinline__ ProductArgs product_of_group(const GroupedProductArgs
 
 // Few rows a group: a workgroup owns 16 rows of one group and 64 columns, its
 // four waves take every fourth chunk of the contraction straight from memory, and
-// the partial tiles are added in wave order through LDS. Bound by the latency of
-// its few loads.
+// the partial tiles are added in wave order through LDS. Bound by latency: the
+// group, then the rows' indexes, then rows and matrix, one after the other (21 rows in
+// 64 groups, 128 x 128 float: 7.4 us in a trace; a call is bound by the host, 8.2).
+constexpr int kThinRows = 32768;  // of the grid's second dimension
 template <typename T, Dense D>
-__global__ void __launch_bounds__(256) grouped_thin_kernel(const GroupedProductArgs ga, const int ncol)
+__global__ void __launch_bounds__(256) grouped_thin_kernel(const GroupedProductArgs ga, const int tiles)
 {
     __shared__ f32x4 part[3][4][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int tile = blockIdx.x / ncol, n0 = (blockIdx.x % ncol) * 64;
+    const int tile = blockIdx.z * kThinRows + blockIdx.y, n0 = blockIdx.x * 64;
+    if (tile >= tiles)
+        return;  // the whole workgroup
     TileWalk at;
     at.start(ga.gr, 4, tile, tile + 1);
     if (at.n == 0)
@@ -80,7 +83,9 @@ __global__ void __launch_bounds__(256) grouped_thin_kernel(const GroupedProductA
 // of as many tiles as it has waves. It keeps its columns of one group's matrix in
 // LDS while its waves walk that group's tiles, each on its own; at the next group
 // the matrix is laid out anew, between two barriers. The next tile's rows are in
-// flight during this one's products, and the row indexes of the one after it.
+// flight during this one's products, and the row indexes of the one after it. HBM
+// bounds it: 441172 x 64 x 64 float in 4 groups with residual and z 119 us, 3.8 TB/s
+// through an order, 112 us where the rows lie in groups (a large copy: 5.0 TB/s).
 // Waves a SIMD that its registers allow: the rows in flight and their parts grow
 // with the contraction (a kernel that takes a few registers more than 128 or 168
 // runs a wave less, and the last workgroups in a second round).
@@ -183,7 +188,13 @@ __global__ void __launch_bounds__((256 * kResidentWaves<T, D, KC>), (kResidentWa
 // group and 128 columns (64 or 32 where the result has no more, the waves one
 // below the other) and takes the contraction in chunks of 64 (32 where the rows
 // have three parts), rows and matrix through LDS, one chunk there while the next
-// is on its way in registers.
+// is on its way in registers. 32768 x 512 x 512 bf16 in 64 groups: 45 us without
+// activation and z, 61 with GELU and z. What bounds it: 440 MB of operands that 64-row
+// tiles take from L2, at the 10 TB/s that no form of this kernel passed, and the
+// epilogue, which few workgroups a compute unit overlap in part only. Tried, and no
+// faster: 128-row tiles (2.3 rounds of workgroups; 71 us), operands straight into LDS
+// without registers (62), the same through several tiles as one sequence (70: two
+// workgroups a compute unit are too few for the epilogue).
 template <typename T, Dense D, int RT, int kCols>
 __global__ void __launch_bounds__(256, kCols == 128 ? 2 : kCols == 64 ? 3 : 4)
     grouped_stream_kernel(const GroupedProductArgs ga, const int ncol, const int tiles)
@@ -384,8 +395,9 @@ hipError_t launch_grouped_product(const GroupedProductArgs &a, hipStream_t strea
     const int64_t tiles = (a.p.M >> 4) + a.gr.n, nc = (a.p.ND + 63) / 64;
     const bool is_float = sizeof(T) == 4, lies = a.p.KD <= 128;
     if (tiles * nc <= (lies ? 2048 : 128) || rows < (lies ? (is_float ? 64 : 32) : (is_float ? 48 : 0))) {
-        hipLaunchKernelGGL((grouped_thin_kernel<T, D>), dim3(static_cast<unsigned>(tiles * nc)), dim3(256), 0, stream, a,
-                           static_cast<int>(nc));
+        const dim3 grid(static_cast<unsigned>(nc), static_cast<unsigned>(tiles < kThinRows ? tiles : kThinRows),
+                        static_cast<unsigned>((tiles + kThinRows - 1) / kThinRows));
+        hipLaunchKernelGGL((grouped_thin_kernel<T, D>), grid, dim3(256), 0, stream, a, static_cast<int>(tiles));
         return hipGetLastError();
     }
     // (d is kept for layers of more than 128 inputs and outputs only)

@@ -17,7 +17,15 @@ namespace etp {
 // A group that lies in one run is written straight to gW and gb. Of one that
 // crosses runs each leaves a partial set, at most two a run: set 2 s of what began
 // in an earlier run, set 2 s + 1 of what goes on in the next; they are added in
-// that order by grouped_join_kernel.
+// that order by grouped_join_kernel. (Runs of whole panels, not of whole groups: ends
+// moved to the nearer group's end save the parts and lose as much to uneven runs.)
+//
+// 5172508 x 64 x 64 bf16 in 16 groups without activation: 411 us, 4.8 TB/s, a copy's
+// rate. 131072 x 64 x 128 float in 25 groups: 66 us, 3.1 TB/s (forming parts, LDS and
+// products of one workgroup a compute unit take turns). 32768 x 512 x 512 bf16 in 64
+// groups with SiLU: d 29, gx 73, gW 123 us and the join 17; one product of d's three
+// parts is 17 us at the matrix rate, so that LDS, vector work and latency bound it.
+// (d kept as parts and brought straight into LDS: gW 103, but gx 88 and d 31.)
 struct GroupedPanelArgs {
     LinearVjpArgs v;  // W, gW, gb of group 0
     Groups gr;

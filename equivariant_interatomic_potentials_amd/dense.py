@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 
+import numpy
 import torch
 
 from .etp import (ETP_BF16, ETP_F32, ETP_FLAG_ACCUMULATE, EtpError, _check, lib)  # noqa: F401
@@ -347,20 +348,36 @@ class TensorList:
     (no ``set_`` or ``.data`` in between)."""
 
     def __init__(self, tensors):
-        self.tensors = tuple(tensors)
-        n = len(self.tensors)
-        self.items, self.pointers = (etp_tensor * max(n, 1))(), (ctypes.c_void_p * max(n, 1))()
-        self.n, self.shape = n, [(t.dtype, t.numel()) for t in self.tensors]
-        spans = []
-        for i, t in enumerate(self.tensors):
-            p = _dense(t, f"tensor {i}", t.dtype, t.numel())
-            self.items[i] = etp_tensor(p, t.numel(), _code(t.dtype))
-            self.pointers[i] = p
-            if t.numel():
-                spans.append((p, p + t.numel() * t.element_size()))
-        _share_device(*self.tensors) if n else None
-        spans.sort()
-        self.apart = all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        ts = self.tensors = tuple(tensors)
+        codes = [_CODE.get(t.dtype) for t in ts]
+        devices = {t.get_device() for t in ts}
+        if None in codes or -1 in devices or not all([t.is_contiguous() for t in ts]):
+            for i, t in enumerate(ts):  # says which
+                _code(t.dtype)
+                _dense(t, f"tensor {i}", t.dtype, t.numel())
+        if len(devices) > 1:
+            raise ValueError(f"tensors of one call must share a device, got {sorted(devices)}")
+        # etp_tensor as three words (the type in the low half of the last); their data on its own as `out`
+        n = self.n = len(ts)
+        self.table = numpy.empty((n, 3), dtype=numpy.int64)
+        self._data = numpy.array([t.data_ptr() for t in ts], dtype=numpy.int64)
+        self.table[:, 0], self.table[:, 1], self.table[:, 2] = self._data, [t.numel() for t in ts], codes
+        self.items, self.pointers = self.table.ctypes.data, self._data.ctypes.data
+        self._shape, self._apart = self.table[:, 1:].tobytes(), None
+
+    @property
+    def apart(self):
+        """Whether no two of the tensors share memory."""
+        if self._apart is None:
+            size = self.table[:, 1] << numpy.where(self.table[:, 2] == ETP_F32, 2, 1)
+            first = self.table[size > 0, 0]
+            order = numpy.argsort(first)
+            self._apart = bool((first[order][1:] >= (first + size[size > 0])[order][:-1]).all())
+        return self._apart
+
+    def like(self, other):
+        """Whether the types and sizes are another list's."""
+        return self._shape == other._shape
 
 
 def _tensor_list(tensors):
@@ -388,7 +405,7 @@ def etp_clip_grads(grads, max_norm: float, out=None, norm=None, ws=None, stream=
     etp_grad_norm_workspace(grads) bytes."""
     g = _tensor_list(grads)
     o = g if out is None else _tensor_list(out)
-    if o.shape != g.shape:
+    if not o.like(g):
         raise ValueError("out must hold tensors of the types and sizes of grads")
     if not o.apart:
         raise ValueError("the clipped tensors overlap")

@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 
+import numpy
 import pytest
 import torch
 
@@ -148,15 +149,34 @@ def test_binding_refuses_host_and_mismatched_tensors():
         dense.TensorList([x])
     with pytest.raises(ValueError, match="contiguous"):
         dense.TensorList([W[:, :, 0]])
-    with pytest.raises(ValueError, match="types and sizes"):
-        dense.etp_clip_grads([], 1.0, _sized_list(3))
+    with pytest.raises(ValueError, match="features must be"):
+        dense.TensorList([ptr])
 
 
-def _sized_list(n):
-    """A list that claims a tensor without owning one (the refusal comes before any use of it)."""
+def listed(*rows):
+    """A list that claims tensors (address, entries, type) without owning any."""
     t = dense.TensorList([])
-    t.shape = [(torch.float32, n)]
+    t.n, t.table = len(rows), numpy.array(rows, dtype=numpy.int64).reshape(-1, 3)
+    t._shape = t.table[:, 1:].tobytes()
     return t
+
+
+def test_gradient_lists():
+    """The list is etp_tensor's layout, and knows whether its tensors share memory."""
+    assert ctypes.sizeof(dense.etp_tensor) == 24 and dense.etp_tensor.dtype.offset == 16
+    t = listed((256, 10, 0), (4096, 7, 1))
+    item = ctypes.cast(t.table.ctypes.data, ctypes.POINTER(dense.etp_tensor))[1]
+    assert (item.data, item.numel, item.dtype) == (4096, 7, 1)
+    assert t.like(listed((0, 10, 0), (8, 7, 1))) and not t.like(listed((256, 10, 0)))
+    assert not t.like(listed((256, 10, 0), (4096, 7, 0))) and not t.like(listed((256, 11, 0), (4096, 7, 1)))
+    assert listed().apart and listed((256, 10, 0)).apart
+    assert listed((296, 10, 1), (256, 10, 0), (316, 1, 0)).apart  # 40, 20 and 4 bytes side by side
+    assert not listed((295, 10, 1), (256, 10, 0)).apart and not listed((256, 10, 0), (256, 10, 0)).apart
+    assert listed((256, 10, 0), (256, 0, 0), (260, 0, 1)).apart
+    with pytest.raises(ValueError, match="types and sizes"):
+        dense.etp_clip_grads([], 1.0, listed((256, 3, 0)))
+    with pytest.raises(ValueError, match="overlap"):
+        dense.etp_clip_grads(listed((256, 3, 0), (260, 3, 0)), 1.0)
 
 
 def test_every_launch_is_checked():
