@@ -375,6 +375,18 @@ __device__ __forceinline__ void store_sums(const GroupedPanelArgs &p, int64_t g,
 {
     const LinearVjpArgs &a = p.v;
     const int64_t nw = p.set - (a.gb ? a.N : 0);
+    if (i + 4 <= nw) {
+        float *o = a.gW + g * nw + i, sum[8] = {v[0], v[1], v[2], v[3]};
+        if (add) {
+            float was[8];
+            load_n<4>(o, 4, was);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                sum[k] += was[k];
+        }
+        store_n<4>(o, 4, sum);
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (i + k < p.set) {
