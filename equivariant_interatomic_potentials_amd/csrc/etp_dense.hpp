@@ -1,6 +1,6 @@
 // etp_dense.hpp -- device code and launchers shared by the dense operators
-// (linear layer, layer norm, orthogonalised update): typed loads and stores,
-// activations, launch declarations.
+// (linear layer, layer norm, grouped layer, orthogonalised update): typed loads
+// and stores, activations, launch declarations.
 #pragma once
 #include <hip/hip_runtime.h>
 

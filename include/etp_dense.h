@@ -7,7 +7,9 @@
  * takes per-edge features h "from the hidden layers of a radial network" and
  * its VJP hands back grad_h. These calls are those hidden layers -- a linear
  * layer with bias, activation and residual, and the layer norm -- with their
- * VJPs, and the orthogonalised update of a weight matrix (of these layers, of
+ * VJPs, the linear layer with a matrix for each group of rows (an element, a
+ * pair of elements), the norm of all gradients with clipping, and the
+ * orthogonalised update of a weight matrix (of these layers, of
  * W_r, or of the channel-mixing blocks). There is no VJP of the VJPs here: a
  * loss on forces, which differentiates grad_x of these layers once more, needs
  * the caller's own second pass through them (etp_edge_conv_vjp2_radial is that
