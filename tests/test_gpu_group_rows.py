@@ -58,6 +58,16 @@ def test_padding_and_empty_groups(M, G):
     check(np.full(M, G - 1), G)
 
 
+@pytest.mark.parametrize("G", [6, 7, 300, 65535])
+@pytest.mark.parametrize("M", [3, 1023, 1024, 8191, 8192, 8193, 30011])
+def test_long_runs_of_empty_groups(M, G):
+    """Runs of empty groups in front, behind and between, shorter and longer than a lane or a wave writes at once."""
+    say("group_rows empty runs", M, G)
+    for at in ([0], [G - 1], [4, 5], [0, 4, G - 1], [0, 5, G - 1], [G // 2], [1, 65 % G, 131 % G, G // 3]):
+        check(np.resize(np.array(at, dtype=np.int64), M), G)
+        check(np.resize(np.array(at + [-1, G], dtype=np.int64), M), G)
+
+
 @pytest.mark.parametrize("M,G", [(5172508, 100), (3000001, 1000)])
 def test_many_rows(M, G):
     say("group_rows many", M, G)
