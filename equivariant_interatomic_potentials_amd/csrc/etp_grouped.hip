@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(256) grouped_thin_kernel(const GroupedProductA
 // LDS while its waves walk that group's tiles, each on its own; at the next group
 // the matrix is laid out anew, between two barriers. The next tile's rows are in
 // flight during this one's products, and the row indexes of the one after it. HBM
-// bounds it: 441172 x 64 x 64 float in 4 groups with residual and z 119 us, 3.8 TB/s
-// through an order, 112 us where the rows lie in groups (a large copy: 5.0 TB/s).
+// bounds it: 441172 x 64 x 64 float in 4 groups with residual and z 111 us, 4.1 TB/s
+// through an order, 107 us where the rows lie in groups (a large copy: 5.0 TB/s).
 // Waves a SIMD that its registers allow: the rows in flight and their parts grow
 // with the contraction (a kernel that takes a few registers more than 128 or 168
 // runs a wave less, and the last workgroups in a second round).
@@ -350,7 +350,7 @@ static hipError_t launch_resident_product(const GroupedProductArgs &a, hipStream
     runs = runs < most ? runs : most < 1 ? 1 : most;
     // few groups: large teams, whose tiles lie side by side at any time, at the price
     // of a matrix laid out by every workgroup of a team (441172 x 64 x 64 float in 4
-    // groups: 119 us in 8 teams, 123 in 64; in 1: 104 and 114); many: each on its own
+    // groups: 107 us in 8 teams, 115 in 64; in 1: 104 and 110); many: each on its own
     // (in 1000 groups: 215 us in 8 teams, 128 in 1024; in 64 to 100 both alike)
     int teams = a.gr.n <= 32 ? 8 : runs;
     teams = teams < runs ? teams : runs;

@@ -47,7 +47,7 @@ __device__ __forceinline__ int group_of_tile(const Groups &gr, int shift, int ti
 }
 
 // A walk over the tiles from number `tile` to `stop`: the slots slot .. slot + n
-// - 1 of group g, n = 0 behind the last one.
+// - 1 of group g, n = 0 behind the last one. Called by whole waves.
 struct TileWalk {
     int g, begin, end, tile, slot, n;
 
@@ -74,6 +74,23 @@ struct TileWalk {
     __device__ __forceinline__ int last_tile(int shift) const { return first_tile(shift) + ((end - begin - 1) >> shift); }
 
 private:
+    // From an empty group on to the next one with rows, if one starts before `stop`: 64
+    // groups a step. (Taken one by one in the loop below, empty groups cost the others too:
+    // 441172 x 64 x 64 float in 4 groups, none empty, 120 us, so 111.)
+    __device__ __forceinline__ bool pass_empty(const Groups &gr, int shift, int stop)
+    {
+        for (; g < gr.n && first_tile(shift) < stop; g += 64) {
+            const int i = g + (threadIdx.x & 63);
+            const uint64_t some = __ballot(i < gr.n && group_start(gr, i + 1) > group_start(gr, i));
+            if (some) {
+                g += __builtin_ctzll(some);
+                begin = group_start(gr, g);
+                end = group_start(gr, g + 1);
+                return true;
+            }
+        }
+        return false;
+    }
     __device__ __forceinline__ void settle(const Groups &gr, int shift, int stop)
     {
         for (;;) {
@@ -88,6 +105,8 @@ private:
             begin = end;
             const int e = group_start(gr, g + 1);
             end = e > begin ? e : begin;
+            if (end == begin && !pass_empty(gr, shift, stop))
+                return;
             const int own = first_tile(shift);
             tile = tile > own ? tile : own;
             if (tile >= stop)

@@ -166,6 +166,26 @@ def test_group_boundaries(sizes, K, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 700, 9000])
+@pytest.mark.parametrize("K,N", [(64, 48), (200, 150)])
+def test_long_runs_of_empty_groups(rows, K, N, dtype):
+    """Groups with rows behind 62, 63, 64, 65 and 500 empty ones: one run of tiles meets several, or ends in one."""
+    import numpy as np
+    import torch
+    say("empty runs", rows, K, N, dtype)
+    sizes = [5] + [0] * 62 + [129] + [0] * 63 + [rows] + [0] * 64 + [3] + [0] * 65 + [rows] + [0] * 500 + [2, 0, 1] + [0] * 130
+    M, G = sum(sizes), len(sizes)
+    p = make(M, G, K, N, dtype, rows + K)
+    ptr = torch.from_numpy(np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)).cuda()
+    p.update(ptr=ptr, order=torch.randperm(M, generator=torch.Generator().manual_seed(3)).int().cuda())
+    y, z = run_fwd(p, "silu", M, N)
+    o7 = out(M, N, p["dt"])
+    for g, r in zip((y, z), want_fwd(p, "silu", o7, o7)):
+        ref.close(g, r)
+    close_vjp(run_vjp(p, "silu", M, K, N), p, "silu", out(M, K, p["dt"]))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("M,G,K,N", [(70001, 4, 64, 64), (70001, 40, 64, 128), (40000, 3, 128, 30), (50000, 100, 20, 96),
                                      (33000, 5, 300, 128), (20000, 64, 256, 256), (30000, 2, 136, 512),
                                      (12000, 1, 512, 136), (60000, 700, 48, 33)])
