@@ -170,7 +170,7 @@ ETP_API etp_status etp_group_rows_workspace(int64_t n_rows, int32_t n_groups, si
  * r = s, rows that lie in groups). Features stay in the caller's row order.
  * W [n_groups][n_in][n_out]; bias float [n_groups][n_out] or NULL; everything
  * else as etp_linear. Rows in no group (before group_ptr[0], behind
- * group_ptr[n_groups]) are neither read nor written. group_ptr, order: DEVICE
+ * group_ptr[n_groups]) have no effect and are not written. group_ptr, order: DEVICE
  * int32, as etp_group_rows writes them, and trusted: a row named twice is written
  * twice, in any order (an index that is no row is passed over, offsets outside [0,
  * n_rows] are held to that range). The sizes of the groups are not read back;
@@ -226,11 +226,12 @@ ETP_API etp_status etp_grad_norm(int32_t n_tensors, const etp_tensor *grads, flo
 
 /* Clipping to a largest norm: with norm as above (kept in double),
  *   out[i][e] = grads[i][e] * (norm <= max_norm ? 1 : max_norm / norm)
- * rounded once. out: HOST array of DEVICE pointers, each of its tensor's type,
- * dense, equal to its tensor's data (in place) or apart from every tensor of the
- * call; NULL: all in place. In place nothing is written when the norm is small
- * enough. An infinite norm gives zeros (NaN from the infinite entries), a NaN
- * makes every entry NaN: *norm tells. norm: DEVICE float, written when not NULL.
+ * rounded once (a bf16's scale and product are floats first). out: HOST array of
+ * DEVICE pointers, each of its tensor's type, dense, equal to its tensor's data (in
+ * place) or apart from every tensor of the call; NULL: all in place. In place nothing
+ * is written when the norm is small enough. An infinite norm gives zeros (NaN from the
+ * infinite entries), a NaN makes every entry NaN: *norm tells. norm: DEVICE float,
+ * written when not NULL.
  * max_norm: finite, >= 0. ws as etp_grad_norm. Errors: as etp_grad_norm (norm may
  * be NULL), plus INVALID_ARGUMENT (max_norm, an out[i] that is null with entries
  * or misaligned). */
