@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import operator
+import weakref
 
 import numpy
 import torch
@@ -365,17 +366,34 @@ class TensorList:
         self._data = numpy.array(list(map(T.data_ptr, ts)), dtype=numpy.int64)
         self.table[:, 0], self.table[:, 1], self.table[:, 2] = self._data, list(map(T.numel, ts)), codes
         self.items, self.pointers = self.table.ctypes.data, self._data.ctypes.data
-        self._shape, self._apart = self.table[:, 1:].tobytes(), None
+        self._shape, self._apart, self._clear_of = self.table[:, 1:].tobytes(), None, None
+
+    def _sizes(self):
+        return self.table[:, 1] << numpy.where(self.table[:, 2] == ETP_F32, 2, 1)
 
     @property
     def apart(self):
         """Whether no two of the tensors share memory."""
         if self._apart is None:
-            size = self.table[:, 1] << numpy.where(self.table[:, 2] == ETP_F32, 2, 1)
+            size = self._sizes()
             first = self.table[size > 0, 0]
             order = numpy.argsort(first)
             self._apart = bool((first[order][1:] >= (first + size[size > 0])[order][:-1]).all())
         return self._apart
+
+    def clear_of(self, grads):
+        """Whether each of these tensors, which are apart, is the one of its place in grads (a list of the same types and
+        sizes) or shares memory with none of that list."""
+        if self._clear_of is None or self._clear_of() is not grads:
+            size = self._sizes()
+            mine, theirs, size = self.table[size > 0, 0], grads.table[size > 0, 0], size[size > 0]
+            order = numpy.argsort(mine)
+            first, end = mine[order], (mine + size)[order]
+            met = first.searchsorted(theirs + size) - end.searchsorted(theirs, "right")
+            if (met > (mine == theirs)).any():
+                return False
+            self._clear_of = weakref.ref(grads)
+        return True
 
     def like(self, other):
         """Whether the types and sizes are another list's."""
@@ -403,14 +421,16 @@ def etp_grad_norm(grads, norm, ws=None, stream=None):
 
 def etp_clip_grads(grads, max_norm: float, out=None, norm=None, ws=None, stream=None):
     """out[i] = grads[i] * min(1, max_norm / norm) with the norm of etp_grad_norm, which is written to norm (float, one
-    element) when given. out: a TensorList or tensors of the same types and sizes, or None: in place. ws:
-    etp_grad_norm_workspace(grads) bytes."""
+    element) when given. out: a TensorList or tensors of the same types and sizes, or None: in place. Each output is its own
+    gradient or shares memory with no gradient and no other output. ws: etp_grad_norm_workspace(grads) bytes."""
     g = _tensor_list(grads)
     o = g if out is None else _tensor_list(out)
     if not o.like(g):
         raise ValueError("out must hold tensors of the types and sizes of grads")
     if not o.apart:
         raise ValueError("the clipped tensors overlap")
+    if o is not g and not o.clear_of(g):
+        raise ValueError("the clipped tensors overlap gradients other than their own")
     wp, wb = _workspace(ws)
     np_ = _dense(norm, "norm", torch.float32, 1, True)
     first = [t for t in (*g.tensors[:1], *o.tensors[:1], norm, ws) if t is not None]
