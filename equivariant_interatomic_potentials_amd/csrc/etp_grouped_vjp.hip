@@ -495,7 +495,9 @@ static void cut_runs(GroupedCut &v, int64_t M, int G, int K, int N, int shift, i
     s = s < 1 ? 1 : s;
     v.per = static_cast<int>((v.tiles + s - 1) / s);
     v.runs = (v.tiles + v.per - 1) / v.per;
-    v.part_bytes = sizeof(float) * 2 * static_cast<size_t>(v.runs) * (static_cast<size_t>(K) + 1) * N;
+    // (of one run every group's sums go straight to the gradients)
+    const size_t sets = v.runs > 1 ? 2 * static_cast<size_t>(v.runs) : 0;
+    v.part_bytes = sizeof(float) * sets * (static_cast<size_t>(K) + 1) * N;
     v.part_bytes = (v.part_bytes + 15) / 16 * 16;
 }
 
