@@ -20,6 +20,12 @@ namespace etp {
 // that order by grouped_join_kernel. (Runs of whole panels, not of whole groups: ends
 // moved to the nearer group's end save the parts and lose as much to uneven runs.)
 //
+// The sums of a long group are no one chain of float additions: the matrix instruction
+// drops what lies below its accumulator's last place, always to the same side, so that
+// 100000 rows in one accumulator were 8e-4 of the result off where all terms are alike
+// (the atoms of a crystal). After `fold` panels they are added to the sums so far,
+// where the group's go, and parts are joined in double: 1.7e-5 at any number of rows.
+//
 // 5172508 x 64 x 64 bf16 in 16 groups without activation: 411 us, 4.8 TB/s, a copy's
 // rate. 131072 x 64 x 128 float in 25 groups: 66 us, 3.1 TB/s (forming parts, LDS and
 // products of one workgroup a compute unit take turns). 32768 x 512 x 512 bf16 in 64
@@ -34,6 +40,7 @@ struct GroupedPanelArgs {
     int runs;
     int nkb, blocks;  // blocks along K, and in all
     int64_t set;      // floats of a partial set: gW, then gb, of those that are wanted
+    int fold;         // panels of a chain
 };
 
 // Parts of x and d, waves, LDS rows (elements), buffers, panel rows, LDS bytes
@@ -258,7 +265,8 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
     if (then.n > 0)
         after.next(p.gr, S.shift, stop);
     int rows_after = rows_of(after);
-    while (at.n > 0) {  // a group; the registers hold its first panel
+    bool begun = false;  // the group has sums already
+    while (at.n > 0) {   // a group, or `fold` panels of it; the registers hold the first
         const int g = at.g;
         const bool whole = at.first_tile(S.shift) >= from && at.last_tile(S.shift) < stop;
         const int set = 2 * s + (at.first_tile(S.shift) >= from ? 1 : 0);
@@ -290,8 +298,9 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
             if (then.n > 0)
                 fetch(rows_then);
         }
+        int left = p.fold;
         for (bool same = true; same;) {
-            same = then.n > 0 && then.g == g;
+            same = then.n > 0 && then.g == g && --left > 0;
             if constexpr (S.bufs == 1) {
                 put(lds);
                 if (then.n > 0)
@@ -319,33 +328,52 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
             if constexpr (S.bufs == 1)
                 lds_barrier();  // the next panel overwrites the rows
         }
-        // the group's sums
+        // the group's sums, or what they grow by
         float *gw = nullptr, *gbias = nullptr;
-        bool add = false;
+        bool add = begun;
         if (whole) {
             gw = want_gw ? a.gW + static_cast<int64_t>(g) * K * N : nullptr;
             gbias = want_gb ? a.gb + static_cast<int64_t>(g) * N : nullptr;
-            add = a.accumulate;
+            add |= a.accumulate;
         } else {
             float *part = static_cast<float *>(a.ws) + set * p.set;
             gw = part;
             gbias = part + p.set - N;
         }
         if (want_gw) {
+            // the lane's first entry, opaque: else the places and masks of all its entries are
+            // formed once for all groups and held in registers through the panels
+            int kl = k0 + 16 * kt0 + 4 * q, jl = j0 + 16 * jt0 + c;
+            asm volatile("" : "+v"(kl), "+v"(jl));
+            if (add) {
+                // read together, a row of tiles at a time; past the matrix anything (not stored)
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    float was[JT][4];
+#pragma unroll
+                    for (int j = 0; j < JT; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int k = kl + 16 * i + r, jj = jl + 16 * j;
+                            was[j][r] = gw[k < K && jj < N ? static_cast<int64_t>(k) * N + jj : 0];
+                        }
+#pragma unroll
+                    for (int j = 0; j < JT; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[i][j][r] += was[j][r];
+                }
+            }
 #pragma unroll
             for (int i = 0; i < KT; ++i)
 #pragma unroll
-                for (int j = 0; j < JT; ++j) {
-                    const int jj = j0 + 16 * (jt0 + j) + c;
+                for (int j = 0; j < JT; ++j)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int k = k0 + 16 * (kt0 + i) + 4 * q + r;
-                        if (k < K && jj < N) {
-                            float *o = gw + static_cast<int64_t>(k) * N + jj;
-                            *o = add ? *o + acc[i][j][r] : acc[i][j][r];
-                        }
+                        const int k = kl + 16 * i + r, jj = jl + 16 * j;
+                        if (k < K && jj < N)
+                            gw[static_cast<int64_t>(k) * N + jj] = acc[i][j][r];
                     }
-                }
         }
         if (want_gb) {
             // the threads that share columns, through LDS, in row order
@@ -367,6 +395,7 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
             if constexpr (S.bufs == 1)
                 lds_barrier();  // the next group's panel overwrites the sums
         }
+        begun = at.n > 0 && at.g == g;
     }
 }
 
@@ -396,15 +425,15 @@ __device__ __forceinline__ void store_sums(const GroupedPanelArgs &p, int64_t g,
 }
 
 // Adds the parts of the groups that cross runs, `span` entries a workgroup, four a
-// lane at a time, every wave a quarter of the parts in order; and zeroes the
-// gradients of groups without rows. Where there are few groups, row y of the grid is
+// lane at a time, every wave a quarter of the parts in order, in double (there may be
+// thousands); and zeroes the gradients of groups without rows. Where there are few groups, row y of the grid is
 // group y; else rows up to runs - 1 are the boundaries between runs, and a boundary
 // stands for the group that crosses it if that crosses no earlier one, and the other
 // rows look for groups without rows (25 groups in 512 runs by boundaries: 18 us, of
 // which most find their group and leave; by groups 5).
 __global__ void __launch_bounds__(256) grouped_join_kernel(const GroupedPanelArgs p, const int shift, const int by_group, const int span)
 {
-    __shared__ float lds[3][64][4];
+    __shared__ double lds[3][64][4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t from = static_cast<int64_t>(blockIdx.x) * span, stop = from + span < p.set ? from + span : p.set;
     auto zero = [&](int g) {
@@ -437,7 +466,7 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(const GroupedPanelArg
         const int64_t i = i0 + 4 * lane;
         const float *part = static_cast<const float *>(p.v.ws) + i;
         const int valid = stop - i < 4 ? static_cast<int>(stop - i) : 4;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        double v[4] = {0.0, 0.0, 0.0, 0.0};
         if (valid > 0) {
 #pragma unroll 4
             for (int r = run0 + wave; r <= run1; r += 4) {
@@ -457,10 +486,11 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(const GroupedPanelArg
         }
         lds_barrier();
         if (wave == 0 && valid > 0) {
+            float sum[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                v[k] = (v[k] + lds[0][lane][k]) + (lds[1][lane][k] + lds[2][lane][k]);
-            store_sums(p, g, i, v, p.v.accumulate);
+                sum[k] = static_cast<float>((v[k] + lds[0][lane][k]) + (lds[1][lane][k] + lds[2][lane][k]));
+            store_sums(p, g, i, sum, p.v.accumulate);
         }
     }
 }
@@ -471,14 +501,23 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(const GroupedPanelArg
 struct GroupedCut {
     bool fused, keep_d;
     int kc, nc, nkb, nnb;
-    int shift, tiles, per, runs;
+    int shift, tiles, per, runs, fold;
     size_t d_bytes, part_bytes;
 };
 
+// Panels of a chain: at most 256 results of matrix instructions on top of each other
+// (32 rows take six in a float layer, three in a bf16 one, one without an activation).
+// Shorter ones cost: with half of it 5172508 x 64 x 64 bf16 takes 8 us more.
+static int chain_panels(bool bf16, bool plain, int shift)
+{
+    return (!bf16 ? 1344 : plain ? 8192 : 2688) >> shift;
+}
+constexpr int kChains = 32;  // of a group in one run
+
 // Runs for a tile size and a number of workgroups that run at once: as many as those
 // (one more would double the time), or over up to four rounds where that fills them
-// better by a tenth.
-static void cut_runs(GroupedCut &v, int64_t M, int G, int K, int N, int shift, int per_cu)
+// better by a tenth; more where one would take a group in more than kChains chains.
+static void cut_runs(GroupedCut &v, int64_t M, int G, int K, int N, int shift, int per_cu, int chain)
 {
     v.shift = shift;
     v.tiles = static_cast<int>((M >> shift) + G);
@@ -491,10 +530,16 @@ static void cut_runs(GroupedCut &v, int64_t M, int G, int K, int N, int shift, i
             rounds = n;
         }
     }
+    // panels that one group may have, and in a run of as many chains as may be
+    const int most = static_cast<int>((M - 1) >> shift) + 1, run = kChains * chain;
+    const int64_t least = most > run ? (v.tiles + run - 1) / run : 1;
+    s = s < least ? least : s;
     s = s < v.tiles ? s : v.tiles;
-    s = s < 1 ? 1 : s;
     v.per = static_cast<int>((v.tiles + s - 1) / s);
     v.runs = (v.tiles + v.per - 1) / v.per;
+    // chains of like length
+    const int longest = v.per < most ? v.per : most, chains = (longest + chain - 1) / chain;
+    v.fold = (longest + chains - 1) / chains;
     // (of one run every group's sums go straight to the gradients)
     const size_t sets = v.runs > 1 ? 2 * static_cast<size_t>(v.runs) : 0;
     v.part_bytes = sizeof(float) * sets * (static_cast<size_t>(K) + 1) * N;
@@ -511,7 +556,7 @@ static GroupedCut grouped_cut(int64_t M, int G, int K, int N, bool bf16, bool pl
     v.nnb = (N + 127) / 128;
     v.fused = K <= 128 && N <= 128;
     const GroupedShape shape(bf16, v.kc, v.nc, plain);
-    cut_runs(v, M, G, K, N, shape.shift, shape.per_cu);
+    cut_runs(v, M, G, K, N, shape.shift, shape.per_cu, chain_panels(bf16, plain, shape.shift));
     v.keep_d = K > 128 && N > 128 && !plain;
     v.d_bytes = v.keep_d ? (sizeof(float) * static_cast<size_t>(M) * N + 15) / 16 * 16 : 0;
     return v;
@@ -610,7 +655,7 @@ static hipError_t grouped_vjp(const GroupedLinearVjpArgs &ga, hipStream_t stream
     const int64_t set = (a.gW ? static_cast<int64_t>(a.K) * a.N : 0) + (a.gb ? a.N : 0);
     hipError_t e = hipSuccess;
     GroupedCut v{};
-    GroupedPanelArgs p{a, gr, nullptr, 0, 1, 1, 1, 1, set};
+    GroupedPanelArgs p{a, gr, nullptr, 0, 1, 1, 1, 1, set, 1};
     if (a.M > 0) {
         v = grouped_cut(a.M, gr.n, a.K, a.N, bf16, plain);
         if (!a.gW && !(v.fused && a.gx)) {
@@ -620,6 +665,7 @@ static hipError_t grouped_vjp(const GroupedLinearVjpArgs &ga, hipStream_t stream
         p.tiles = v.tiles;
         p.per = v.per;
         p.runs = v.runs;
+        p.fold = v.fold;
         p.nkb = v.nkb;
         p.blocks = v.nkb * v.nnb;
         if (!v.fused || set == 0) {

@@ -7,7 +7,7 @@ from equivariant_interatomic_potentials_amd import dense
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("rows,groups,n_in,n_out", [(2, 1, 65536, 16384), (1, 1, 64, 64), (31, 1, 128, 128),
-                                                    (5000, 40, 4096, 4096), (300, 3, 2048, 2048)])
+                                                    (900, 40, 4096, 4096), (300, 3, 2048, 2048)])
 def test_one_run_needs_no_partial_sums(rows, groups, n_in, n_out, dtype):
     """What is left is d (float), which layers of more than 128 inputs and outputs keep, and the bias gradient's parts
     where it is asked for alone: two for each run, of which there are at most rows / 32 + groups."""
