@@ -84,7 +84,8 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
     const int s = id / p.blocks, blk = id % p.blocks;
     const int k0 = (blk % p.nkb) * 32 * KC, j0 = (blk / p.nkb) * 32 * NC;
     const int K = a.K, N = a.N;
-    const bool want_gx = a.gx != nullptr, want_gw = a.gW != nullptr, want_gb = a.gb != nullptr && k0 == 0;
+    // (d is kept where gx is a product of its own)
+    const bool want_gx = !FromD && a.gx != nullptr, want_gw = a.gW != nullptr, want_gb = a.gb != nullptr && k0 == 0;
     const int from = s * p.per, stop = from + p.per < p.tiles ? from + p.per : p.tiles;
 
     // loads: a thread takes 16 bytes of the same columns in every RD-th (RX-th)
