@@ -23,8 +23,8 @@ namespace etp {
 // The sums of a long group are no one chain of float additions: the matrix instruction
 // drops what lies below its accumulator's last place, always to the same side, so that
 // 100000 rows in one accumulator were 8e-4 of the result off where all terms are alike
-// (the atoms of a crystal). After `fold` panels they are added to the sums so far,
-// where the group's go, and parts are joined in double: 1.7e-5 at any number of rows.
+// (the atoms of a crystal). After `fold` panels they are added to the sums so far, and
+// parts are joined in double: 1.7e-5 at any number of rows.
 //
 // 5172508 x 64 x 64 bf16 in 16 groups without activation: 411 us, 4.8 TB/s, a copy's
 // rate. 131072 x 64 x 128 float in 25 groups: 66 us, 3.1 TB/s (forming parts, LDS and
@@ -139,8 +139,28 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
     // gW: waves as WK x WN, each KT x JT tiles of 16 x 16
     constexpr int WN = W == 4 || NC == 1 ? 2 : 4, WK = W / WN, KT = 2 * KC / WK, JT = 2 * NC / WN;
     const int kt0 = (wave / WN) * KT, jt0 = (wave % WN) * JT;
-    f32x4 acc[KT][JT];
-    float gb[VD];
+    // The chains of a group are added up in registers where a block is 128 x 128 (two waves
+    // a SIMD; through memory 65536 x 512 x 512 float in 8 groups takes 607 us, so 594), else
+    // where the group's sums go (in registers 441172 x 64 x 64 bf16 takes 78 us, so 74).
+    constexpr bool kHolds = KC == 4 && NC == 4;
+    f32x4 acc[KT][JT], held[kHolds ? KT : 1][kHolds ? JT : 1];
+    float gb[VD], gb_held[VD];
+    auto end_chain = [&](bool first) __attribute__((always_inline)) {
+        if constexpr (kHolds) {
+#pragma unroll
+            for (int i = 0; i < KT; ++i)
+#pragma unroll
+                for (int j = 0; j < JT; ++j) {
+                    held[i][j] = first ? acc[i][j] : held[i][j] + acc[i][j];
+                    acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+#pragma unroll
+            for (int i = 0; i < VD; ++i) {
+                gb_held[i] = first ? gb[i] : gb_held[i] + gb[i];
+                gb[i] = 0.f;
+            }
+        }
+    };
 
     // the fetched panel's parts into LDS
     auto put = [&](bf16bits *dl) __attribute__((always_inline)) {
@@ -266,8 +286,8 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
     if (then.n > 0)
         after.next(p.gr, S.shift, stop);
     int rows_after = rows_of(after);
-    bool begun = false;  // the group has sums already
-    while (at.n > 0) {   // a group, or `fold` panels of it; the registers hold the first
+    bool begun = false;  // the group has sums in memory
+    while (at.n > 0) {   // a group, or a chain of it; the registers hold the first panel
         const int g = at.g;
         const bool whole = at.first_tile(S.shift) >= from && at.last_tile(S.shift) < stop;
         const int set = 2 * s + (at.first_tile(S.shift) >= from ? 1 : 0);
@@ -292,16 +312,16 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
 #pragma unroll
         for (int i = 0; i < VD; ++i)
             gb[i] = 0.f;
-        int buf = 0;
+        end_chain(true);
+        int buf = 0, left = p.fold;
         if constexpr (S.bufs == 2) {
             lds_barrier();  // of the group before: its sums or its last panel
             put(lds);
             if (then.n > 0)
                 fetch(rows_then);
         }
-        int left = p.fold;
         for (bool same = true; same;) {
-            same = then.n > 0 && then.g == g && --left > 0;
+            same = then.n > 0 && then.g == g && (kHolds || left > 1);
             if constexpr (S.bufs == 1) {
                 put(lds);
                 if (then.n > 0)
@@ -318,6 +338,10 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
             }
             products(lds + buf * kBuf, rows);
             buf ^= S.bufs - 1;
+            if (--left == 0) {
+                end_chain(false);
+                left = p.fold;
+            }
             at = then;
             rows = rows_then;
             then = after;
@@ -330,6 +354,16 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
                 lds_barrier();  // the next panel overwrites the rows
         }
         // the group's sums, or what they grow by
+        if constexpr (kHolds) {
+#pragma unroll
+            for (int i = 0; i < KT; ++i)
+#pragma unroll
+                for (int j = 0; j < JT; ++j)
+                    acc[i][j] += held[i][j];
+#pragma unroll
+            for (int i = 0; i < VD; ++i)
+                gb[i] += gb_held[i];
+        }
         float *gw = nullptr, *gbias = nullptr;
         bool add = begun;
         if (whole) {
@@ -396,7 +430,7 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
             if constexpr (S.bufs == 1)
                 lds_barrier();  // the next group's panel overwrites the sums
         }
-        begun = at.n > 0 && at.g == g;
+        begun = !kHolds && at.n > 0 && at.g == g;
     }
 }
 
