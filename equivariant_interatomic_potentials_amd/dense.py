@@ -366,30 +366,36 @@ class TensorList:
         self._data = numpy.array(list(map(T.data_ptr, ts)), dtype=numpy.int64)
         self.table[:, 0], self.table[:, 1], self.table[:, 2] = self._data, list(map(T.numel, ts)), codes
         self.items, self.pointers = self.table.ctypes.data, self._data.ctypes.data
-        self._shape, self._apart, self._clear_of = self.table[:, 1:].tobytes(), None, None
+        self._shape = self.table[:, 1:].tobytes()
+        self._memory = self._apart = self._clear_of = None
 
-    def _sizes(self):
-        return self.table[:, 1] << numpy.where(self.table[:, 2] == ETP_F32, 2, 1)
+    def _spans(self):
+        """Addresses and bytes of the tensors that are not empty."""
+        if self._memory is None:
+            size = self.table[:, 1] << 2 - (self.table[:, 2] != ETP_F32)
+            live = size.nonzero()[0]
+            self._memory = self.table[live, 0], size[live]
+        return self._memory
 
     @property
     def apart(self):
         """Whether no two of the tensors share memory."""
         if self._apart is None:
-            size = self._sizes()
-            first = self.table[size > 0, 0]
-            order = numpy.argsort(first)
-            self._apart = bool((first[order][1:] >= (first + size[size > 0])[order][:-1]).all())
+            first, size = self._spans()
+            order = first.argsort()
+            self._sorted = first[order], (first + size)[order]
+            self._apart = bool((self._sorted[0][1:] >= self._sorted[1][:-1]).all())
         return self._apart
 
     def clear_of(self, grads):
-        """Whether each of these tensors, which are apart, is the one of its place in grads (a list of the same types and
-        sizes) or shares memory with none of that list."""
+        """Whether the tensors are apart, and each is the one of its place in grads (a list of the same types and sizes) or
+        shares memory with none of that list."""
+        if not self.apart:
+            return False
         if self._clear_of is None or self._clear_of() is not grads:
-            size = self._sizes()
-            mine, theirs, size = self.table[size > 0, 0], grads.table[size > 0, 0], size[size > 0]
-            order = numpy.argsort(mine)
-            first, end = mine[order], (mine + size)[order]
-            met = first.searchsorted(theirs + size) - end.searchsorted(theirs, "right")
+            mine, size = self._spans()
+            theirs = grads._spans()[0]
+            met = self._sorted[0].searchsorted(theirs + size) - self._sorted[1].searchsorted(theirs, "right")
             if (met > (mine == theirs)).any():
                 return False
             self._clear_of = weakref.ref(grads)
