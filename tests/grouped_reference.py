@@ -48,10 +48,12 @@ def linear_vjp(x, W, gy, ptr, order=None, z=None, name="none", gx0=None):
 def linear_vjp_terms(x, W, gy, ptr, order=None, z=None, name="none"):
     """Largest 2-norm of the terms of one entry of gx, gW and gb.
 
-    The bar of a float sum. A sum of n terms t_i in float errs by at most (n - 1) 2^-24 sum |t_i| <= n^1.5 2^-24 |t| and,
-    its roundings having either sign, by about sqrt(n) 2^-24 times a partial sum, which is about |t|: at n = 100 000
-    that is 2e-5 |t| at the very most in one chain, and 1e-5 |t| bounds it for the chains of at most 64 rows that these
-    kernels join. Where terms cancel the sum itself is far smaller than |t| and no bar."""
+    The bar of a float sum whose terms have either sign. The kernels add at most 256 results of the matrix instruction
+    on top of each other, which drops up to a unit (2^-23) of the partial sum each time, half of one on average and to
+    the same side. A partial sum of i terms of n is about sqrt(i / n) |t|, so that 256 results lose about
+    2 / 3 * 256 * 2^-24 |t| = 1e-5 |t| of their chain, and a gradient of several chains, or one of fewer results, less.
+    (Terms of one sign have a larger bound of their own: test_gpu_grouped_sums.) Where terms cancel the sum itself is
+    far smaller than |t| and no bar."""
     M, (G, K, N) = gy.shape[0], W.shape
     x, gy, z = ref.f64(x), ref.f64(gy), ref.f64(z)
     most = [0.0, 0.0, 0.0]

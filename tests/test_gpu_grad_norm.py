@@ -3,8 +3,8 @@ once to float: within 2^-24 of the float64 norm (and the summation's 2^-50 or
 so, which 2^-40 covers). A
 clipped float is the product with a double scale rounded once: half a step
 of the result, 2^-24 relative, plus the scale's own rounding; a bf16 one is formed in
-float from a float scale and rounded to bf16: 2^-9 (1 + 2^-22) relative at most, for
-which 2^-8 is allowed."""
+float from a float scale (2^-23 at most) and rounded to bf16: half a step is at most
+2^-8 / (1 + 2^-8) < 2^-8 - 2^-17 of the value, so that 2^-8 holds both."""
 import math
 
 import pytest
