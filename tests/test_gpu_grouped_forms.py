@@ -49,3 +49,19 @@ def test_accumulates_where_parts_are_joined_by_boundaries(act, dtype):
     got = base.run_vjp(p, act, M, K, N, flags=etp.ETP_FLAG_ACCUMULATE, base=to)
     for t, b, r in zip(got, was, base.want_vjp(p, act, torch.zeros(M, K))):
         ref.close(t, b + r)
+
+
+@pytest.mark.parametrize("K,N", [(64, 64), (200, 300)])
+def test_infinite_bf16_gradients_without_activation(K, N):
+    """d is grad_y as it is, one part: an infinity stays one, as in IEEE arithmetic."""
+    import torch
+    M, G = 400, 4
+    base.say("grouped infinite", K, N)
+    p = base.make(M, G, K, N, "bf16", 4, pad=0)
+    row = int(p["order"][int(p["ptr"][2])])  # the first row of group 2
+    p["gy"][row, 1] = float("-inf")
+    got = base.run_vjp(p, "none", M, K, N)
+    for g, r in zip(got, base.want_vjp(p, "none", base.out(M, K, p["dt"]))):
+        ref.close(g, r)
+        inf = torch.isinf(r)
+        assert inf.any() and torch.equal(ref.f64(g)[inf], r[inf])
