@@ -88,7 +88,9 @@ __global__ void __launch_bounds__(256) grouped_thin_kernel(const GroupedProductA
 // through an order, 107 us where the rows lie in groups (a large copy: 5.0 TB/s).
 // Waves a SIMD that its registers allow: the rows in flight and their parts grow
 // with the contraction (a kernel that takes a few registers more than 128 or 168
-// runs a wave less, and the last workgroups in a second round).
+// runs a wave less, and the last workgroups in a second round). Two are held to that by
+// a few registers in scratch memory: float forward of 33 to 64 entries, 28 bytes a lane,
+// and of 97 to 128, 36.
 template <typename T, Dense D, int KC>
 constexpr int kResidentWaves = sizeof(T) == 4 ? (D == Dense::Gx ? (KC == 1 ? 4 : KC == 2 ? 3 : 2) : KC <= 2 ? 4 : 3)
                                               : (D == Dense::Gx && KC > 2 ? 3 : 4);
@@ -189,10 +191,11 @@ __global__ void __launch_bounds__((256 * kResidentWaves<T, D, KC>), (kResidentWa
 // below the other) and takes the contraction in chunks of 64 (32 where the rows
 // have three parts), rows and matrix through LDS, one chunk there while the next
 // is on its way in registers. 32768 x 512 x 512 bf16 in 64 groups: 45 us without
-// activation and z, 61 with GELU and z. What bounds it: 440 MB of operands that 64-row
-// tiles take from L2, at the 10 TB/s that no form of this kernel passed, and the
-// epilogue, which few workgroups a compute unit overlap in part only. Tried, and no
-// faster: 128-row tiles (2.3 rounds of workgroups; 71 us), operands straight into LDS
+// activation and z, 61 with GELU and z. No unit is full: of 160 thousand cycles LDS is
+// busy for 61 (22 of them bank conflicts), vector instructions for 54, matrix ones for
+// 17, and 541 MB pass L2 (8.5 TB/s, 75% hits); waves wait for 47% of theirs, since a
+// workgroup's loads, barriers, products and epilogue take turns and the few workgroups
+// of a compute unit overlap them in part only. Tried, and no faster: 128-row tiles (2.3 rounds of workgroups; 71 us), operands straight into LDS
 // without registers (62), the same through several tiles as one sequence (70: two
 // workgroups a compute unit are too few for the epilogue).
 template <typename T, Dense D, int RT, int kCols>

@@ -27,11 +27,18 @@ namespace etp {
 // parts are joined in double: 1.7e-5 at any number of rows.
 //
 // 5172508 x 64 x 64 bf16 in 16 groups without activation: 411 us, 4.8 TB/s, a copy's
-// rate. 131072 x 64 x 128 float in 25 groups: 66 us, 3.1 TB/s (forming parts, LDS and
-// products of one workgroup a compute unit take turns). 32768 x 512 x 512 bf16 in 64
-// groups with SiLU: d 29, gx 73, gW 123 us and the join 17; one product of d's three
-// parts is 17 us at the matrix rate, so that LDS, vector work and latency bound it.
-// (d kept as parts and brought straight into LDS: gW 103, but gx 88 and d 31.)
+// rate. 131072 x 64 x 128 float in 25 groups: 66 us, 3.1 TB/s; of 162 thousand cycles
+// vector instructions take 48, LDS 36 and matrix instructions 25, and waves wait for 45%
+// of theirs: forming the parts, storing them and the products of one workgroup a compute
+// unit take turns. 32768 x 512 x 512 bf16 in 64 groups with SiLU: d 29, gx 73, gW 119 us
+// and the join 19. gW and gx have three products a term, 13 us each at the matrix rate;
+// in gW's 280 thousand cycles LDS is busy for 107, vector instructions for 74 and matrix
+// ones for 52, again in turns (waves wait for 45%); in gx' 165 LDS for 103, vector
+// instructions for 61, matrix ones for 52. (d kept as parts and brought straight into
+// LDS: gW 103, but gx 88 and d 31.)
+//
+// No instance spills vector registers. (The masks and places of a block's entries, which
+// the compiler forms before the panels if it can, once took 20 to 40 of them.)
 struct GroupedPanelArgs {
     LinearVjpArgs v;  // W, gW, gb of group 0
     Groups gr;
@@ -377,7 +384,8 @@ __global__ void __launch_bounds__((64 * kGroupedShape<T, KC, NC, Plain>.waves),
         }
         if (want_gw) {
             // the lane's first entry, opaque: else the places and masks of all its entries are
-            // formed once for all groups and held in registers through the panels
+            // formed once for all groups and held in registers through the panels (441172 x
+            // 64 x 64 bf16 with SiLU 79 us, so 74)
             int kl = k0 + 16 * kt0 + 4 * q, jl = j0 + 16 * jt0 + c;
             asm volatile("" : "+v"(kl), "+v"(jl));
             if (add) {
